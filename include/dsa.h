@@ -346,6 +346,128 @@ dsa_status dsa_append_kv_mx(const uint16_t *k_new, const uint16_t *latent_new,
                             int32_t n, int32_t DI, int32_t Dqk, uint8_t *k_idx_cache,
                             uint8_t *k_scales, uint16_t *kv_cache, dsa_stream_t stream);
 
+/* ---- rotary positions --------------------------------------------------------------
+ * Layers whose queries and keys carry rotary positions (the 64 rotary elements
+ * of a 576-wide latent row and of its queries; the heads of the local layers).
+ * Pair i of a rotated part of `dim` elements at position p turns by the angle
+ * p * inv_freq[i], formed in fp64 and reduced to one turn before its sine and
+ * cosine are taken in fp32, so far positions lose nothing:
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin);  inverse: sin -> -sin
+ * (with factor 1 the inverse is the transpose: it undoes the rotation, and
+ * takes a gradient through it).  Pairs are elements (i, i + dim/2) of the part
+ * (DSA_ROPE_HALF) or (2i, 2i + 1) (DSA_ROPE_INTERLEAVED).  Elements of a head
+ * outside [offset, offset + dim) are copied.  Results are rounded once, from
+ * fp32. */
+typedef enum { DSA_BF16 = 0, DSA_F16 = 1, DSA_E4M3 = 2 } dsa_dtype;
+enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1 };
+
+typedef struct {
+    const double *inv_freq; /* device fp64 [dim/2]: radians per position */
+    int32_t dim;            /* rotated elements: even, >= 2 */
+    int32_t offset;         /* of the rotated part within a head */
+    int32_t layout;         /* DSA_ROPE_HALF or DSA_ROPE_INTERLEAVED */
+    int32_t inverse;        /* 0 or 1 */
+    float factor;           /* multiplies cosine and sine; finite */
+} dsa_rope_spec;
+
+/* Host-side: inverse frequencies base^(-2i/dim), i < dim/2, for contexts
+ * `scale` times as long as the `orig_len` positions of training, and the
+ * factor that goes with them (1 but for YaRN).  Published schemes:
+ *   DSA_ROPE_PLAIN   unchanged (scale and orig_len are not looked at);
+ *   DSA_ROPE_LINEAR  position interpolation: every frequency / scale;
+ *   DSA_ROPE_NTK     base * scale^(dim/(dim-2)): the slowest pair stretches by
+ *                    scale, the fastest stays (dim > 2);
+ *   DSA_ROPE_YARN    pairs of over 32 turns within orig_len stay, those of under
+ *                    one are divided by scale, a linear ramp over the pair index
+ *                    between (bounds rounded outward); factor 0.1 ln(scale) + 1.
+ * inv_freq_host: host fp64 [dim/2]; factor: host. base > 1, scale >= 1. */
+enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 };
+dsa_status dsa_rope_frequencies(int32_t dim, double base, int32_t scheme, double scale, int32_t orig_len,
+                                double *inv_freq_host, float *factor);
+
+/* Rotates T tokens' queries and, in the same launch, keys.  Element (t, h, d)
+ * of an array lies at t*token_stride + h*head_stride + d elements, so slices of
+ * one fused projection need no copy.
+ *   q      device bf16 or fp16 (dtype), Hq heads of D;  q_out as q; the same
+ *          pointer and strides rotate in place, other overlaps are not allowed
+ *   k      the same with Hk heads, or NULL (Hk = 0)
+ *   pos    device int32 [T]: any value
+ * rope->offset + rope->dim <= D.  Arrays that are 16-byte aligned with strides,
+ * offset and dim/2 multiples of 8 take the vectorised path; others are served
+ * too.  Needs no workspace. */
+dsa_status dsa_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq, void *q_out,
+                    int64_t q_out_token_stride, int64_t q_out_head_stride, const void *k, int64_t k_token_stride,
+                    int64_t k_head_stride, int32_t Hk, void *k_out, int64_t k_out_token_stride,
+                    int64_t k_out_head_stride, const int32_t *pos, int32_t T, int32_t D, int32_t dtype,
+                    const dsa_rope_spec *rope, dsa_stream_t stream);
+
+/* ---- a paged cache of keys and values, and the append that rotates on the way --------
+ * Element (page, row, head, d) of the keys lies at page*k_page_stride +
+ * row*k_row_stride + head*k_head_stride + d elements (any order of pages, rows
+ * and heads; head dimension contiguous); values likewise.  Both bases and all
+ * strides are multiples of 16 bytes; the stride of a dimension of one entry is
+ * not looked at.  DSA_E4M3 caches hold e4m3(value * scale).  v == NULL (Dv = 0):
+ * rows without values of their own, such as the latent rows. */
+typedef struct {
+    void *k, *v; /* device */
+    int64_t k_page_stride, k_row_stride, k_head_stride;
+    int64_t v_page_stride, v_row_stride, v_head_stride;
+    int32_t heads, Dk, Dv;
+    int32_t dtype; /* dsa_dtype */
+    float k_scale, v_scale; /* DSA_E4M3 only: finite, > 0 */
+} dsa_kv_cache;
+
+/* For each new token j, at position tok_pos[j] of sequence tok_seq[j] (through
+ * the block table; already counted in seq_lens), in one launch:
+ *   cache keys   = k_new[j] rotated to tok_pos[j] (rope NULL: unchanged)
+ *   cache values = v_new[j]               (when the cache has values)
+ *   q_out[j]     = q[j] rotated to tok_pos[j]  (q NULL: none; needs rope)
+ * An E4M3 cache gets e4m3(x * scale): x in fp32, one rounding, ties to even,
+ * saturating to +-448.  k_new, v_new, q: device, dtype bf16 or fp16, strides as in
+ * dsa_rope, heads as the cache's (q: H heads of Dk).  A bf16 or fp16 cache has the
+ * inputs' dtype.  tok_seq[j] = -1 marks padding: nothing is written for it.  A
+ * sequence or position out of range, or a page outside [0, num_pages), skips that
+ * token and sets DSA_DEVERR_POSITION / DSA_DEVERR_PAGE.  Tokens must go to distinct
+ * rows.  Supported: Dk, Dv multiples of 16.  Needs no workspace. */
+dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_head_stride, const void *v_new,
+                           int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                           int64_t q_head_stride, int32_t H, void *q_out, int64_t q_out_token_stride,
+                           int64_t q_out_head_stride, const int32_t *tok_seq, const int32_t *tok_pos,
+                           const dsa_paged *pg, int32_t n, int32_t dtype, const dsa_rope_spec *rope,
+                           const dsa_kv_cache *cache, dsa_stream_t stream);
+
+/* ---- attention of each sequence's newest tokens over its paged cache -----------------
+ * Sequence b's queries are rows q_start[b] .. q_start[b+1]-1 of q: its last
+ * n_b = q_start[b+1] - q_start[b] tokens, already in the cache.  The query at
+ * position p attends to positions max(0, p - window + 1) .. p (window = 0: all
+ * of 0 .. p); query head h reads K/V head h / (H / heads):
+ *   l_s = sm_scale * q.k_s,  out = sum_s softmax(l)_s v_s,  lse = ln sum_s exp(l_s)
+ * A query without any position (n_b > seq_lens[b], an empty sequence) gets
+ * out = 0, lse = -inf.  Rows from q_start[num_seqs] on are left as they were.
+ *   q        device bf16 or fp16 (dtype): H heads of Dk, strides as in dsa_rope,
+ *            multiples of 8, 16-byte aligned
+ *   cache    bf16 or fp16 as q, or E4M3; rows at positions below seq_lens must be
+ *            finite, what other rows hold does not matter; with a window, the
+ *            block-table entries of pages before the first needed one are not read
+ *   q_start  device int32 [num_seqs + 1], not decreasing, q_start[num_seqs] <= T; NULL:
+ *            decode, query t is the last token of sequence t, T == num_seqs
+ *   max_q, max_len  host bounds on n_b and seq_lens: a sequence over either, or
+ *            with q_start out of order, is skipped and sets DSA_DEVERR_SHAPE
+ *   out      device dtype [T, H, Dv] dense;  lse device fp32 [T, H] or NULL
+ *   ws       dsa_paged_attn_workspace_bytes() bytes, 256-byte aligned; contents
+ *            need no initialisation; calls that may overlap need one each
+ * A page outside [0, num_pages) reads as zeros and sets DSA_DEVERR_PAGE.
+ * Softmax statistics and sums are fp32; the softmax weights enter the second
+ * product in the q type (fp16 for an E4M3 cache).  Results do not depend on
+ * what else is in the call's timing: no atomics, a fixed order of sums.
+ * Supported: Dk == Dv in {64, 128}, H a multiple of heads. */
+size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, const dsa_kv_cache *cache,
+                                      int32_t max_q, int32_t max_len, int32_t window);
+dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t H,
+                          const dsa_kv_cache *cache, const dsa_paged *pg, const int32_t *q_start, int32_t T,
+                          int32_t max_q, int32_t max_len, int32_t window, float sm_scale, int32_t dtype, void *out,
+                          float *lse, void *ws, size_t ws_bytes, dsa_stream_t stream);
+
 /* ---- testing the bounded waits ------------------------------------------------------
  * Every pipeline wait in the kernels gives up after a time limit (1 s),
  * records DSA_DEVERR_TIMEOUT, lets the CTA's other roles abandon their work,

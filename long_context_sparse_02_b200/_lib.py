@@ -52,6 +52,16 @@ class LayerArgs(ctypes.Structure):
                 ("out", P), ("idx_out", P), ("lse", P), ("q_idx_scales", P), ("k_idx_scales", P)]
 
 
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("inv_freq", P), ("dim", I32), ("offset", I32), ("layout", I32), ("inverse", I32), ("factor", F32)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_page_stride", I64), ("k_row_stride", I64), ("k_head_stride", I64),
+                ("v_page_stride", I64), ("v_row_stride", I64), ("v_head_stride", I64), ("heads", I32), ("Dk", I32),
+                ("Dv", I32), ("dtype", I32), ("k_scale", F32), ("v_scale", F32)]
+
+
 lib.dsa_abi_version.restype = I32
 lib.dsa_abi_version.argtypes = []
 lib.dsa_status_string.restype = ctypes.c_char_p
@@ -101,6 +111,20 @@ lib.dsa_test_skip_indexer_tile.restype = ctypes.c_int
 lib.dsa_test_skip_indexer_tile.argtypes = [I64]
 lib.dsa_swa_decode.restype = ctypes.c_int
 lib.dsa_swa_decode.argtypes = [P, P, P, P, I32, I32, I32, I32, F32, P, P]
+lib.dsa_rope_frequencies.restype = ctypes.c_int
+lib.dsa_rope_frequencies.argtypes = [I32, ctypes.c_double, I32, ctypes.c_double, I32, ctypes.POINTER(ctypes.c_double),
+                                     ctypes.POINTER(F32)]
+lib.dsa_rope.restype = ctypes.c_int
+lib.dsa_rope.argtypes = [P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I32, I32, I32,
+                         ctypes.POINTER(RopeSpec), P]
+lib.dsa_append_rope.restype = ctypes.c_int
+lib.dsa_append_rope.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, P, ctypes.POINTER(Paged), I32,
+                                I32, ctypes.POINTER(RopeSpec), ctypes.POINTER(KvCache), P]
+lib.dsa_paged_attn_workspace_bytes.restype = SZ
+lib.dsa_paged_attn_workspace_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(KvCache), I32, I32, I32]
+lib.dsa_paged_attn.restype = ctypes.c_int
+lib.dsa_paged_attn.argtypes = [P, I64, I64, I32, ctypes.POINTER(KvCache), ctypes.POINTER(Paged), P, I32, I32, I32, I32,
+                               F32, I32, P, P, P, SZ, P]
 
 EXPORTS = ["dsa_abi_version", "dsa_status_string", "dsa_device_error", "dsa_indexer_scores", "dsa_indexer_scores_mx",
            "dsa_append_kv_mx",
@@ -109,7 +133,8 @@ EXPORTS = ["dsa_abi_version", "dsa_status_string", "dsa_device_error", "dsa_inde
            "dsa_layer_workspace_bytes", "dsa_layer_forward", "dsa_layer_forward_profiled",
            "dsa_layer_kernel_launches", "dsa_swa_decode", "dsa_append_kv", "dsa_cp_candidates",
            "dsa_cp_select_workspace_bytes", "dsa_cp_select", "dsa_cp_lse_merge",
-           "dsa_test_skip_indexer_tile"]
+           "dsa_test_skip_indexer_tile", "dsa_rope_frequencies", "dsa_rope", "dsa_append_rope",
+           "dsa_paged_attn_workspace_bytes", "dsa_paged_attn"]
 
 
 def _check(fn: str, status: int):
@@ -340,3 +365,186 @@ def append_kv_mx(k_new, latent_new, tok_seq, tok_pos, pg: Paged, k_cache, k_scal
         _ptr(tok_seq, torch.int32, "tok_seq"), _ptr(tok_pos, torch.int32, "tok_pos"), ctypes.byref(pg), n, DI, Dqk,
         _ptr(k_cache, torch.uint8, "k_cache"), _ptr(k_scales, torch.uint8, "k_scales"),
         _ptr(kv_cache, torch.bfloat16, "kv_cache", True), _stream()))
+
+
+# ---- rotary positions, the rotating append and attention over a paged K/V cache ----------------------------------
+
+BF16, F16, E4M3 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCHEMES = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_IO = {torch.bfloat16: BF16, torch.float16: F16}
+_CACHE = {torch.bfloat16: BF16, torch.float16: F16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}
+
+
+def _on(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _call(fn: str, device: torch.device, *args):
+    """The library call on `device`'s current stream, with that device current."""
+    f = getattr(lib, fn)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+    return _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _heads(t, name: str, dtype=None, heads=None, width=None):
+    """[T, heads, D] with a contiguous last dimension: (pointer, token stride, head stride)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.dtype not in _IO if dtype is None else t.dtype != dtype):
+        raise ValueError(f"{name} must be a {dtype or 'bf16 or fp16'} tensor [tokens, heads, width], got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    if (heads is not None and t.shape[1] != heads) or (width is not None and t.shape[2] != width):
+        raise ValueError(f"{name} must have {heads} heads of {width}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
+def rope_frequencies(dim: int, base: float = 10000.0, scheme: str = "plain", scale: float = 1.0, orig_len: int = 0):
+    """(inverse frequencies, a CPU fp64 tensor [dim/2]; factor): scheme "plain", "linear", "ntk" or "yarn" for contexts
+    `scale` times as long as the `orig_len` of training."""
+    if scheme not in ROPE_SCHEMES:
+        raise ValueError(f"scheme must be one of {sorted(ROPE_SCHEMES)}")
+    freq = torch.empty(max(int(dim) // 2, 1), dtype=torch.float64)
+    factor = F32(1.0)
+    _check("dsa_rope_frequencies", lib.dsa_rope_frequencies(
+        int(dim), float(base), ROPE_SCHEMES[scheme], float(scale), int(orig_len),
+        ctypes.cast(freq.data_ptr(), ctypes.POINTER(ctypes.c_double)), ctypes.byref(factor)))
+    return freq, float(factor.value)
+
+
+def rope_spec(inv_freq: torch.Tensor, offset: int = 0, interleaved: bool = False, inverse: bool = False,
+              factor: float = 1.0) -> RopeSpec:
+    """inv_freq fp64 [dim/2] on the GPU; elements offset .. offset + dim of each head are rotated.  Keeps inv_freq alive."""
+    spec = RopeSpec(_ptr(inv_freq, torch.float64, "inv_freq"), 2 * int(inv_freq.numel()), int(offset),
+                    ROPE_INTERLEAVED if interleaved else ROPE_HALF, int(bool(inverse)), float(factor))
+    spec._tensors = (inv_freq,)
+    return spec
+
+
+def kv_cache(k: torch.Tensor, v: torch.Tensor = None, k_scale: float = 1.0, v_scale: float = 1.0) -> KvCache:
+    """A paged cache [pages, 64, heads, width] of keys and (optionally) values: bf16, fp16, or e4m3 codes of value * scale
+    (uint8 or float8_e4m3fn).  Any strides with a contiguous last dimension.  Keeps both tensors alive."""
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            continue
+        if not t.is_cuda or t.dim() != 4 or t.shape[1] != 64 or t.dtype not in _CACHE or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a CUDA tensor [pages, 64, heads, width] of bf16, fp16 or e4m3 codes with a "
+                             f"contiguous last dimension, got {t.dtype} {tuple(t.shape)}")
+        if t.dtype != k.dtype or t.shape[:3] != k.shape[:3] or t.device != k.device:
+            raise ValueError("k and v must have the same dtype, device, pages and heads")
+    sv = v.stride() if v is not None else (0, 0, 0)
+    c = KvCache(k.data_ptr(), v.data_ptr() if v is not None else None, *k.stride()[:3], *sv[:3], int(k.shape[2]),
+                int(k.shape[3]), int(v.shape[3]) if v is not None else 0, _CACHE[k.dtype], float(k_scale), float(v_scale))
+    c._tensors = (k, v)
+    return c
+
+
+def _cache_fits(cache: KvCache, pg: Paged, device):
+    k = cache._tensors[0]
+    if k.shape[0] < pg.num_pages:
+        raise ValueError(f"the cache has {k.shape[0]} pages, the page table {pg.num_pages}")
+    _on(device, cache=k, seq_lens=pg._tensors[0], block_table=pg._tensors[1])
+
+
+def _tokens(t, name: str, n: int):
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return _ptr(t, torch.int32, name)
+
+
+def rope(q, pos, spec: RopeSpec, k=None, q_out=None, k_out=None):
+    """Rotary positions on q [T, H, D] and (optionally, in the same launch) k [T, Hk, D], bf16 or fp16, at pos int32 [T].
+    q_out / k_out default to new dense tensors; pass q / k themselves to rotate in place.  Returns (q_out, k_out)."""
+    T, H, D = q.shape
+    qa = _heads(q, "q")
+    _on(q.device, pos=pos, k=k, q_out=q_out, k_out=k_out, inv_freq=spec._tensors[0])
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    ka, ko, Hk = (None, 0, 0), (None, 0, 0), 0
+    if k is not None:
+        ka, Hk = _heads(k, "k", q.dtype, width=D, heads=k.shape[1]), int(k.shape[1])
+        if k.shape[0] != T:
+            raise ValueError("k must have q's tokens")
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        ko = _heads(k_out, "k_out", q.dtype)
+    _call("dsa_rope", q.device, *qa, H, *_heads(q_out, "q_out", q.dtype), *ka, Hk, *ko, _tokens(pos, "pos", T), T, D,
+          _IO[q.dtype], ctypes.byref(spec))
+    return q_out, k_out
+
+
+def append_rope(k_new, v_new, tok_seq, tok_pos, pg: Paged, cache: KvCache, spec: RopeSpec = None, q=None, q_out=None):
+    """k_new [n, heads, Dk] (rotated to tok_pos) and v_new [n, heads, Dv] or None into the cache; q [n, H, Dk], where given,
+    rotated in the same launch into q_out (default: a new dense tensor; q itself for in place), which is returned."""
+    n = k_new.shape[0]
+    ka = _heads(k_new, "k_new", None, cache.heads, cache.Dk)
+    dtype, dev = k_new.dtype, k_new.device
+    _on(dev, v_new=v_new, tok_seq=tok_seq, tok_pos=tok_pos, q=q, q_out=q_out)
+    _cache_fits(cache, pg, dev)
+    va = (None, 0, 0)
+    if v_new is not None:
+        if v_new.shape[0] != n:
+            raise ValueError("v_new must have k_new's tokens")
+        va = _heads(v_new, "v_new", dtype, cache.heads, cache.Dv)
+    qa, qo, H = (None, 0, 0), (None, 0, 0), 0
+    if q is not None:
+        if q.shape[0] != n:
+            raise ValueError("q must have k_new's tokens")
+        H = int(q.shape[1])
+        qa = _heads(q, "q", dtype, H, cache.Dk)
+        if q_out is None:
+            q_out = torch.empty((n, H, cache.Dk), dtype=dtype, device=dev)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qo = _heads(q_out, "q_out", dtype)
+    if spec is not None:
+        _on(dev, inv_freq=spec._tensors[0])
+    _call("dsa_append_rope", dev, *ka, *va, *qa, H, *qo, _tokens(tok_seq, "tok_seq", n), _tokens(tok_pos, "tok_pos", n),
+          ctypes.byref(pg), n, _IO[dtype], ctypes.byref(spec) if spec is not None else None, ctypes.byref(cache))
+    return q_out if q is not None else None
+
+
+def paged_attn_workspace(T: int, H: int, cache: KvCache, pg: Paged, max_q: int, max_len: int, window: int = 0):
+    """A workspace for paged_attn calls of at most these sizes, on the cache's device."""
+    dev = cache._tensors[0].device
+    with torch.cuda.device(dev):
+        need = int(lib.dsa_paged_attn_workspace_bytes(int(T), pg.num_seqs, int(H), ctypes.byref(cache), int(max_q),
+                                                      int(max_len), int(window)))
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+
+
+def paged_attn(q, cache: KvCache, pg: Paged, q_start, max_q: int, max_len: int, window: int = 0, sm_scale: float = None,
+               want_lse: bool = False, out=None, lse=None, ws=None):
+    """Attention of q [T, H, D], each sequence's newest tokens (rows q_start[b] .. q_start[b+1], int32 [num_seqs + 1]; None:
+    one each), over the paged cache, causal, optionally within a window.  Returns out, or (out, lse) with want_lse."""
+    T, H, D = q.shape
+    qa = _heads(q, "q", None, H, cache.Dk)
+    dev = q.device
+    _on(dev, q_start=q_start, out=out, lse=lse, ws=ws)
+    _cache_fits(cache, pg, dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be dense, with q's shape and dtype")
+    if lse is None and want_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    elif lse is not None and tuple(lse.shape) != (T, H):
+        raise ValueError(f"lse must be [{T}, {H}]")
+    if ws is None:
+        ws = paged_attn_workspace(T, H, cache, pg, max_q, max_len, window)
+    _call("dsa_paged_attn", dev, *qa, H, ctypes.byref(cache), ctypes.byref(pg),
+          None if q_start is None else _tokens(q_start, "q_start", pg.num_seqs + 1), T, max_q, max_len, window,
+          D ** -0.5 if sm_scale is None else sm_scale, _IO[q.dtype], out.data_ptr(),
+          _ptr(lse, torch.float32, "lse", True), ws.data_ptr(), ws.numel())
+    return (out, lse) if lse is not None else out

@@ -105,6 +105,19 @@ bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, cons
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_4d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, const uint64_t dims[4],
+                  const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle swz) {
+    CUtensorMap probe;
+    if (!make_tmap_2d(&probe, base, dt, dims[0], dims[1], strides[0], box[0], box[1], swz)) return false;  // loads the encoder
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) d[i] = dims[i], b[i] = box[i];
+    for (int i = 0; i < 3; ++i) st[i] = strides[i];
+    if (dims[2] == 0 || dims[3] == 0) return false;
+    return g_encode(m, dt, 4, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dsa
 
 using namespace dsa;
@@ -124,6 +137,40 @@ bool hi_ok(int HI) { return HI == 4 || HI == 8 || HI == 16 || HI == 32 || HI == 
 bool attn_shape_ok(int Dqk, int Dv) { return (Dqk == 576 && Dv == 512) || (Dqk == 64 && Dv == 64); }
 
 size_t ld_of(int32_t max_len) { return align_up((size_t)max_len, 4); }
+
+bool io_dtype_ok(int32_t dtype) { return dtype == DSA_BF16 || dtype == DSA_F16; }
+
+dsa_status rope_spec_check(const dsa_rope_spec *r, int32_t D) {
+    if (!r || !r->inv_freq || r->dim < 2 || (r->dim & 1) || r->offset < 0 || r->dim > D || r->offset > D - r->dim ||
+        !isfinite(r->factor) || (r->inverse != 0 && r->inverse != 1) ||
+        (r->layout != DSA_ROPE_HALF && r->layout != DSA_ROPE_INTERLEAVED))
+        return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+// A stride of the cache, in elements: positive and a multiple of 16 bytes
+// unless its dimension has one entry; below 2^40 bytes (a tensor map's limit).
+bool cache_stride_ok(int64_t stride, int64_t entries, int elem) {
+    return entries <= 1 || (stride > 0 && (stride * elem) % 16 == 0 && stride < ((int64_t)1 << 39));
+}
+
+dsa_status kv_cache_check(const dsa_kv_cache *c, const dsa_paged *pg) {
+    if (!c || !c->k || c->heads < 1 || c->Dk < 1 || c->Dv < 0 || (c->v != nullptr) != (c->Dv > 0))
+        return DSA_ERR_INVALID_ARG;
+    if (!io_dtype_ok(c->dtype) && c->dtype != DSA_E4M3) return DSA_ERR_INVALID_ARG;
+    if (c->dtype == DSA_E4M3 &&
+        (!isfinite(c->k_scale) || c->k_scale <= 0 || (c->v && (!isfinite(c->v_scale) || c->v_scale <= 0))))
+        return DSA_ERR_INVALID_ARG;
+    const int e = c->dtype == DSA_E4M3 ? 1 : 2;
+    if (!aligned16(c->k) || !cache_stride_ok(c->k_page_stride, pg->num_pages, e) ||
+        !cache_stride_ok(c->k_row_stride, 64, e) || !cache_stride_ok(c->k_head_stride, c->heads, e))
+        return DSA_ERR_INVALID_ARG;
+    if (c->v && (!aligned16(c->v) || !cache_stride_ok(c->v_page_stride, pg->num_pages, e) ||
+                 !cache_stride_ok(c->v_row_stride, 64, e) || !cache_stride_ok(c->v_head_stride, c->heads, e)))
+        return DSA_ERR_INVALID_ARG;
+    if ((c->Dk | c->Dv) % 16) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
 
 struct LayerWs {
     uint32_t *score_hist;  // decode: the indexer's per-query score histogram (kept zeroed between calls)
@@ -464,6 +511,112 @@ dsa_status dsa_swa_decode(const uint16_t *q, const uint16_t *k_ring, const uint1
     if (!aligned16(q) || !aligned16(k_ring) || !aligned16(v_ring) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     SwaArgs a{q, k_ring, v_ring, seq_lens, B, H, D, window, sm_scale, out};
     return launch_swa(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_rope_frequencies(int32_t dim, double base, int32_t scheme, double scale, int32_t orig_len,
+                                double *inv_freq_host, float *factor) {
+    if (dim < 2 || (dim & 1) || !(base > 1) || !isfinite(base) || !inv_freq_host || !factor) return DSA_ERR_INVALID_ARG;
+    if (scheme < DSA_ROPE_PLAIN || scheme > DSA_ROPE_YARN) return DSA_ERR_INVALID_ARG;
+    if (scheme != DSA_ROPE_PLAIN && (!(scale >= 1) || !isfinite(scale))) return DSA_ERR_INVALID_ARG;
+    if (scheme == DSA_ROPE_NTK && dim == 2) return DSA_ERR_INVALID_ARG;
+    if (scheme == DSA_ROPE_YARN && orig_len < 1) return DSA_ERR_INVALID_ARG;
+    const int half = dim / 2;
+    if (scheme == DSA_ROPE_NTK) base *= pow(scale, (double)dim / (dim - 2));
+    *factor = scheme == DSA_ROPE_YARN ? (float)(0.1 * log(scale) + 1.0) : 1.f;
+    // the pair index that turns `turns` times within orig_len positions
+    auto pair_of = [&](double turns) { return half * log(orig_len / (turns * 2 * M_PI)) / log(base); };
+    double lo = 0, hi = 0;
+    if (scheme == DSA_ROPE_YARN) {
+        lo = std::max(floor(pair_of(32)), 0.0);
+        hi = std::min(ceil(pair_of(1)), (double)dim - 1);
+    }
+    for (int i = 0; i < half; ++i) {
+        double f = pow(base, -(double)i / half);
+        if (scheme == DSA_ROPE_LINEAR) f /= scale;
+        if (scheme == DSA_ROPE_YARN) {
+            const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+            f = f * (1 - ramp) + f / scale * ramp;
+        }
+        inv_freq_host[i] = f;
+    }
+    return DSA_OK;
+}
+
+dsa_status dsa_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq, void *q_out,
+                    int64_t q_out_token_stride, int64_t q_out_head_stride, const void *k, int64_t k_token_stride,
+                    int64_t k_head_stride, int32_t Hk, void *k_out, int64_t k_out_token_stride,
+                    int64_t k_out_head_stride, const int32_t *pos, int32_t T, int32_t D, int32_t dtype,
+                    const dsa_rope_spec *rope, dsa_stream_t stream) {
+    if (T < 0 || Hq < 0 || Hk < 0 || D < 2 || !io_dtype_ok(dtype)) return DSA_ERR_INVALID_ARG;
+    if (dsa_status s = rope_spec_check(rope, D)) return s;
+    if (T == 0 || (Hq == 0 && Hk == 0)) return DSA_OK;
+    if (!pos || (Hq && (!q || !q_out)) || (Hk && (!k || !k_out))) return DSA_ERR_INVALID_ARG;
+    // in place means element for element
+    if (Hq && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
+        return DSA_ERR_INVALID_ARG;
+    if (Hk && k == k_out && (k_token_stride != k_out_token_stride || k_head_stride != k_out_head_stride))
+        return DSA_ERR_INVALID_ARG;
+    RopeArgs a{{q, q_token_stride, q_head_stride, Hq},
+               {k, k_token_stride, k_head_stride, Hk},
+               {q_out, q_out_token_stride, q_out_head_stride},
+               {k_out, k_out_token_stride, k_out_head_stride},
+               pos, T, D, dtype, rope};
+    return launch_rope(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_head_stride, const void *v_new,
+                           int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+                           int64_t q_head_stride, int32_t H, void *q_out, int64_t q_out_token_stride,
+                           int64_t q_out_head_stride, const int32_t *tok_seq, const int32_t *tok_pos,
+                           const dsa_paged *pg, int32_t n, int32_t dtype, const dsa_rope_spec *rope,
+                           const dsa_kv_cache *cache, dsa_stream_t stream) {
+    if (n < 0 || H < 0 || !paged_ok(pg) || !io_dtype_ok(dtype)) return DSA_ERR_INVALID_ARG;
+    if (dsa_status s = kv_cache_check(cache, pg)) return s;
+    if (cache->dtype != DSA_E4M3 && cache->dtype != dtype) return DSA_ERR_INVALID_ARG;
+    if (rope)
+        if (dsa_status s = rope_spec_check(rope, cache->Dk)) return s;
+    if ((q != nullptr) != (H > 0) || (q && (!rope || !q_out))) return DSA_ERR_INVALID_ARG;
+    if (q && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
+        return DSA_ERR_INVALID_ARG;
+    if ((v_new != nullptr) != (cache->v != nullptr)) return DSA_ERR_INVALID_ARG;
+    if (n == 0) return DSA_OK;
+    if (!k_new || !tok_seq || !tok_pos) return DSA_ERR_INVALID_ARG;
+    AppendRopeArgs a{{k_new, k_token_stride, k_head_stride, cache->heads},
+                     {v_new, v_token_stride, v_head_stride, v_new ? cache->heads : 0},
+                     {q, q_token_stride, q_head_stride, H},
+                     {q_out, q_out_token_stride, q_out_head_stride},
+                     tok_seq, tok_pos, paged_dev(pg), n, dtype, rope, cache};
+    return launch_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, const dsa_kv_cache *cache, int32_t max_q,
+                                      int32_t max_len, int32_t window) {
+    if (T <= 0 || num_seqs <= 0 || H <= 0 || !cache || cache->heads <= 0 || H % cache->heads || max_q <= 0 ||
+        max_len <= 0 || window < 0)
+        return 0;
+    const DeviceInfo *dev = current_device();
+    return paged_attn_workspace_bytes(T, num_seqs, H, cache->heads, cache->Dk, cache->dtype, max_q, max_len, window,
+                                      dev ? dev->sm_count : 148);
+}
+
+dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t H,
+                          const dsa_kv_cache *cache, const dsa_paged *pg, const int32_t *q_start, int32_t T,
+                          int32_t max_q, int32_t max_len, int32_t window, float sm_scale, int32_t dtype, void *out,
+                          float *lse, void *ws, size_t ws_bytes, dsa_stream_t stream) {
+    if (T < 0 || H < 1 || max_q < 1 || max_len < 1 || window < 0 || !paged_ok(pg) || !isfinite(sm_scale) ||
+        !io_dtype_ok(dtype))
+        return DSA_ERR_INVALID_ARG;
+    if (dsa_status s = kv_cache_check(cache, pg)) return s;
+    if (cache->dtype != DSA_E4M3 && cache->dtype != dtype) return DSA_ERR_INVALID_ARG;
+    if (!q_start && (T != pg->num_seqs)) return DSA_ERR_INVALID_ARG;
+    if (!cache->v || cache->Dk != cache->Dv || (cache->Dk != 64 && cache->Dk != 128) || H % cache->heads)
+        return DSA_ERR_UNSUPPORTED;
+    if (T == 0) return DSA_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+    if ((T > 1 && (q_token_stride & 7)) || (H > 1 && (q_head_stride & 7))) return DSA_ERR_INVALID_ARG;
+    PagedAttnArgs a{{q, q_token_stride, H > 1 ? q_head_stride : 0, H}, cache, paged_dev(pg), q_start, T, max_q,
+                    max_len, window, dtype, sm_scale, out, lse, ws, ws_bytes};
+    return launch_paged_attn(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -31,6 +31,12 @@ bool make_tmap_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint
 bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, const uint64_t dims[3], uint64_t stride1,
                   uint64_t stride2, const uint32_t box[3], CUtensorMapSwizzle swz);
 
+// Builds a 4-D tiled tensor map: dims[0] elements innermost, then dims[1..3]
+// `strides[0..2]` bytes apart (each a multiple of 16); box[0..3].  Reads
+// outside the dimensions fill with zeros.
+bool make_tmap_4d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, const uint64_t dims[4],
+                  const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle swz);
+
 // Raises the dynamic shared-memory limit of `fn` once per device.
 bool ensure_smem(const void *fn, int bytes);
 
@@ -163,6 +169,53 @@ struct AppendArgs {
 dsa_status launch_append(const AppendArgs &a, cudaStream_t st);
 // MXFP8 keys: codes into k_cache, one E8M0 scale per 32 elements into k_scales [pages, 64, DI/32].
 dsa_status launch_append_mx(const AppendArgs &a, uint8_t *k_scales, cudaStream_t st);
+
+// ---- rotary positions, and the append that rotates on the way -------------------------
+// Heads of a call's tokens: element (t, h, d) at data + t*token_stride + h*head_stride + d.
+struct HeadsIn {
+    const void *data;
+    int64_t token_stride, head_stride;
+    int32_t heads;
+};
+struct HeadsOut {
+    void *data;
+    int64_t token_stride, head_stride;
+};
+struct RopeArgs {
+    HeadsIn q, k;  // heads == 0: absent
+    HeadsOut q_out, k_out;
+    const int32_t *pos;
+    int32_t T, D, dtype;
+    const dsa_rope_spec *rope;
+};
+dsa_status launch_rope(const RopeArgs &a, cudaStream_t st);
+struct AppendRopeArgs {
+    HeadsIn k, v, q;  // v.heads, q.heads may be 0
+    HeadsOut q_out;
+    const int32_t *tok_seq, *tok_pos;
+    PagedDev pg;
+    int32_t n, dtype;
+    const dsa_rope_spec *rope;  // NULL: no rotation
+    const dsa_kv_cache *cache;
+};
+dsa_status launch_append_rope(const AppendRopeArgs &a, cudaStream_t st);
+
+// ---- attention of the newest tokens over a paged K/V cache ------------------------------
+struct PagedAttnArgs {
+    HeadsIn q;
+    const dsa_kv_cache *cache;
+    PagedDev pg;
+    const int32_t *q_start;  // NULL: decode, query t is the last token of sequence t
+    int32_t T, max_q, max_len, window, dtype;
+    float sm_scale;
+    void *out;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+};
+size_t paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, int32_t cache_dtype,
+                                  int32_t max_q, int32_t max_len, int32_t window, int sm_count);
+dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st);
 
 // ---- context-parallel decode: joining the ranks' partial results -----------------
 dsa_status launch_cp_candidates(const float *scores, int64_t ld, const int32_t *idx, int B, int K, const int32_t *lo,

@@ -1,0 +1,618 @@
+// Attention of each sequence's newest tokens over its paged K/V cache, for
+// few packed rows a K/V head (single tokens, drafts) and, as 128-row tiles,
+// for any number: warp-level matrix instructions, one pass over the keys with
+// the running maximum and sum of each row.
+//
+//   l_s = c q.k_s,  m = max l,  p_s = 2^(l_s - m),  out = sum p_s v_s / sum p_s
+// with c = sm_scale log2(e), statistics and sums in fp32.
+//
+// With few rows the bound is HBM: a K/V head's keys and values are read once
+// for all its query heads (rows are packed: see paged_plan.cuh).  One CTA per
+// SM: a producer warp keeps a ring of units (64 positions = one page, K and V)
+// full by TMA, 160 KB in flight per SM; eight consumer warps take 16-key
+// slices in turn, each with the running statistics and the output of its 16
+// rows in registers, and join at the end of a tile in a fixed order.  Keys
+// and values go from swizzled shared memory to the fragments by ldmatrix; an
+// 8-bit cache is widened to fp16 (exact) in registers, one conversion for two
+// values, and the rows of q are scaled by a power of two to fit fp16 exactly.
+#include <cuda_fp16.h>
+
+#include "dsa_device.cuh"
+#include "dsa_internal.h"
+#include "paged_plan.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int UNIT = 64;
+constexpr int CW = 8;  // consumer warps
+constexpr int THREADS = (CW + 1) * 32;
+constexpr int RING_BYTES = 160 * 1024;
+constexpr int MERGE_LD = 4;  // floats of padding per merged row
+
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int ELEM = E4M3 ? 1 : 2;
+    static constexpr int ROW_BYTES = D * ELEM;                            // of one head
+    static constexpr int BOX_BYTES = ROW_BYTES < 128 ? ROW_BYTES : 128;   // inner extent of a TMA box
+    static constexpr int BOXES = ROW_BYTES / BOX_BYTES;
+    static constexpr int TILE_BYTES = UNIT * ROW_BYTES;                   // K or V of a unit
+    static constexpr int STAGE = 2 * TILE_BYTES;
+    static constexpr int NST = RING_BYTES / STAGE < 10 ? RING_BYTES / STAGE : 10;
+    static constexpr int MERGE_ROW = D + MERGE_LD;
+    static constexpr int MERGE_BYTES = (CW / 2) * 16 * (MERGE_ROW + 2) * 4;
+    static constexpr int SMEM = NST * STAGE + MERGE_BYTES + 1024;
+};
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of one head:
+// boxes of [64 rows][128 or 64 bytes], swizzled as the tensor map says.
+template <int BOX_BYTES>
+__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
+    if (BOX_BYTES == 128)
+        return (uint32_t)((chunk >> 3) * (UNIT * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t *r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t *r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if (F16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+// Two e4m3 codes (bits 0-15) to fp16 (exact).
+__device__ __forceinline__ uint32_t widen(uint32_t v) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// MT = TM / 16 row groups of 16; the consumer warps are MT row groups x CW/MT
+// key slots.  A unit has four 16-key slices; slot s of a row group takes
+// every (CW/MT)-th slice of the run of units.
+// IO_F16: q and out are fp16 (else bf16).  The matrix products run in fp16
+// when IO_F16 or the cache is E4M3.
+template <int D, bool IO_F16, bool E4M3>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const PagedAttnParams p, const int MT) {
+    using C = Cfg<D, E4M3>;
+    constexpr bool MM_F16 = IO_F16 || E4M3;
+    constexpr int KS = D / 16;  // k-steps of q.k; also pairs of 8-wide output tiles
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *merge = reinterpret_cast<float *>(ring + C::NST * C::STAGE);
+    __shared__ PlanShared plan;
+    __shared__ uint64_t full[C::NST], empty[C::NST];
+    __shared__ int abort_flag;
+    const int warp = warp_id(), lane = lane_id();
+    const int nslot = CW / MT;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::NST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], CW);
+        }
+        abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        p.rec[blockIdx.x].valid = 0;
+    }
+    pdl_trigger();
+    plan_cta<UNIT>(p, blockIdx.x, gridDim.x, plan);  // also orders the barrier setup before its use
+    Cursor cur = plan.cur;
+    Segment g;
+
+    if (warp == CW) {
+        // ---- producer: one unit = one page, K and V of one head ----
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && next_segment<UNIT>(p, cur, g)) {
+            const int hi_unit = (g.x.key_hi + UNIT - 1) / UNIT;
+            for (int u = g.u_begin; ok && u < g.u_end; u += 32) {
+                // page ids of the next 32 units, one a lane
+                int page = p.pg.num_pages;  // outside the map: reads as zeros
+                const int lp = g.x.u0 + u + lane;
+                if (u + lane < g.u_end && lp < hi_unit) {
+                    const int id = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)g.b * p.pg.max_blocks + lp] : -1;
+                    if (id >= 0 && id < p.pg.num_pages)
+                        page = id;
+                    else
+                        record_error(p.err, DSA_DEVERR_PAGE);
+                }
+                const int cnt = min(32, g.u_end - u);
+                for (int i = 0; i < cnt; ++i, ++it) {
+                    const int pg = __shfl_sync(0xffffffffu, page, i);
+                    const int s = it % C::NST;
+                    if (it >= C::NST) ok = mbar_wait(&empty[s], ((it / C::NST) - 1) & 1, p.err, &abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        uint8_t *st = ring + s * C::STAGE;
+                        mbar_expect_tx(&full[s], C::STAGE);
+#pragma unroll
+                        for (int x = 0; x < C::BOXES; ++x) {
+                            const int col = x * (C::BOX_BYTES / C::ELEM);
+                            tma_load_4d(st + x * UNIT * C::BOX_BYTES, &kmap, &full[s], col, 0, g.h, pg);
+                            tma_load_4d(st + C::TILE_BYTES + x * UNIT * C::BOX_BYTES, &vmap, &full[s], col, 0, g.h, pg);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        // copies in flight end before the block's shared memory does (after an
+        // abandoned run; otherwise the consumers have waited for them all)
+        if (!ok)
+            for (uint32_t j = it > C::NST ? it - C::NST : 0; j < it; ++j)
+                mbar_wait(&full[j % C::NST], (j / C::NST) & 1, p.err, nullptr);
+        return;
+    }
+
+    // ---- consumers ----
+    const int rg = warp % MT, slot = warp / MT;
+    const int gid = lane >> 2, tig = lane & 3;
+    uint32_t it = 0;
+    while (next_segment<UNIT>(p, cur, g)) {
+        const int rbase = g.x.row0 + rg * 16;
+        const int last_row = g.x.row0 + g.x.rows;
+        // this thread's two rows: gid and gid + 8 of the group
+        int pos[2];
+        float c[2];
+        uint32_t qf[KS][4];
+        bool have[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = rbase + gid + 8 * r;
+            have[r] = row < last_row;
+            const int tok = row / p.G, hg = row - tok * p.G;
+            pos[r] = have[r] ? g.s.L - g.s.n + tok : -1;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (int64_t)(g.s.q0 + tok) * p.q_token +
+                                  (int64_t)(g.h * p.G + hg) * p.q_head;
+            c[r] = p.scale_log2;
+            if (!E4M3) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    qf[k][r] = have[r] ? *reinterpret_cast<const uint32_t *>(src + k * 16 + tig * 2) : 0;
+                    qf[k][2 + r] = have[r] ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + tig * 2) : 0;
+                }
+            } else {
+                // an 8-bit key fragment holds four consecutive elements a thread: q takes the same order
+                float mx = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint2 v = have[r] ? *reinterpret_cast<const uint2 *>(src + k * 16 + tig * 4) : make_uint2(0, 0);
+                    qf[k][r] = v.x, qf[k][2 + r] = v.y;
+                    const float2 a = unpack2<IO_F16>(v.x), b = unpack2<IO_F16>(v.y);
+                    mx = fmaxf(fmaxf(mx, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+                }
+                if (!IO_F16) {
+                    // bf16 to fp16: times 2^-e with 2^e <= max|q| < 2^(e+1), so that the row fits; what
+                    // is lost lies 2^-24 below the row's largest element
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                    e = mx > 0.f ? max(-126, min(e, 126)) : 0;
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    c[r] *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float2 a = unpack2<false>(qf[k][r + 2 * x]);
+                            qf[k][r + 2 * x] = pack2<true>(a.x * down, a.y * down);
+                        }
+                    }
+                }
+            }
+        }
+        float o[2 * KS][4];
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        auto slice = [&](const uint8_t *st, int key0, int sl) {
+            const uint32_t kb = smem_u32(st), vb = kb + C::TILE_BYTES;
+            float s[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            if (!E4M3) {
+                const int row = sl * 16 + ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4];
+                    ldsm4(b, kb + tile_off<C::BOX_BYTES>(row, 2 * k + ch));
+                    mma16816<MM_F16>(s[0], qf[k], b[0], b[1]);
+                    mma16816<MM_F16>(s[1], qf[k], b[2], b[3]);
+                }
+            } else {
+                const int row = sl * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
+#pragma unroll
+                for (int k = 0; k < KS; k += 2) {
+                    uint32_t b[4];
+                    ldsm4(b, kb + tile_off<C::BOX_BYTES>(row, k + ch));
+                    mma16816<true>(s[0], qf[k], widen(b[0]), widen(b[0] >> 16));
+                    mma16816<true>(s[1], qf[k], widen(b[1]), widen(b[1] >> 16));
+                    mma16816<true>(s[0], qf[k + 1], widen(b[2]), widen(b[2] >> 16));
+                    mma16816<true>(s[1], qf[k + 1], widen(b[3]), widen(b[3] >> 16));
+                }
+            }
+            // scores in log2 units; masked where a row does not see the key
+            const bool edge = key0 + 15 > g.x.p_first || (p.window && key0 <= g.x.p_last - p.window);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = e >> 1;
+                    s[i][e] *= c[r];
+                    if (edge) {
+                        const int key = key0 + i * 8 + tig * 2 + (e & 1);
+                        if (key > pos[r] || (p.window && key <= pos[r] - p.window)) s[i][e] = -INFINITY;
+                    }
+                }
+            float f[2], mu[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                x = fmaxf(x, m[r]);
+                mu[r] = x == -INFINITY ? 0.f : x;
+                f[r] = ex2_approx(m[r] - mu[r]);
+                m[r] = x;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = ex2_approx(s[i][e] - mu[e >> 1]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                l[r] = l[r] * f[r] + ((s[0][2 * r] + s[0][2 * r + 1]) + (s[1][2 * r] + s[1][2 * r + 1]));
+            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                for (int i = 0; i < 2 * KS; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
+            }
+            // weights rounded to the values' type for the second product (their sum l is of the unrounded ones)
+            const uint32_t a[4] = {pack2<MM_F16>(s[0][0], s[0][1]), pack2<MM_F16>(s[0][2], s[0][3]),
+                                   pack2<MM_F16>(s[1][0], s[1][1]), pack2<MM_F16>(s[1][2], s[1][3])};
+            // values at positions that no row of the tile sees may be anything (unwritten rows): taken as 0
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            const bool clear = key0 + 16 > g.x.key_hi || key0 < g.x.key_lo;
+            if (clear) {
+                auto seen = [&](int k) { return k >= g.x.key_lo && k < g.x.key_hi; };
+                const int k = key0 + tig * 2;
+                keep0 = (seen(k) ? 0xffffu : 0u) | (seen(k + 1) ? 0xffff0000u : 0u);
+                keep1 = (seen(k + 8) ? 0xffffu : 0u) | (seen(k + 9) ? 0xffff0000u : 0u);
+            }
+            const int row = sl * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
+            if (!E4M3) {
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    uint32_t b[4];
+                    ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row, 2 * j + ch));
+                    mma16816<MM_F16>(o[2 * j], a, b[0] & keep0, b[1] & keep1);
+                    mma16816<MM_F16>(o[2 * j + 1], a, b[2] & keep0, b[3] & keep1);
+                }
+            } else {
+                // a transposed 16-bit element is two neighbouring elements of one row: o[2j] takes the
+                // even ones of 16, o[2j + 1] the odd ones
+#pragma unroll
+                for (int j = 0; j < KS; j += 2) {
+                    uint32_t b[4];
+                    ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row, j + ch));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t b0 = b[2 * x], b1 = b[2 * x + 1];
+                        mma16816<true>(o[2 * (j + x)], a, widen(__byte_perm(b0, 0, 0x4420)) & keep0,
+                                       widen(__byte_perm(b1, 0, 0x4420)) & keep1);
+                        mma16816<true>(o[2 * (j + x) + 1], a, widen(__byte_perm(b0, 0, 0x4431)) & keep0,
+                                       widen(__byte_perm(b1, 0, 0x4431)) & keep1);
+                    }
+                }
+            }
+        };
+
+        bool ok = true;
+        for (int u = g.u_begin; ok && u < g.u_end; ++u, ++it) {
+            // Every warp waits for and releases every unit, also the ones that the other half of eight slots
+            // takes: a warp that skipped a stage's phase could not tell the one after next by its parity.
+            const int s = it % C::NST;
+            ok = mbar_wait(&full[s], (it / C::NST) & 1, p.err, &abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t *st = ring + s * C::STAGE;
+            const int key0 = (g.x.u0 + u) * UNIT;
+            if (nslot <= 4 || (slot >> 2) == (int)(it & 1))
+                for (int sl = slot & 3; sl < 4; sl += nslot > 4 ? 4 : nslot) slice(st, key0 + sl * 16, sl);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+        }
+        // every consumer warp leaves together when a wait ran out in one of them
+        if (named_bar_or(1, CW * 32, !ok)) return;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        // ---- join the key slots, the upper half into the lower one, in a fixed order ----
+        for (int half = nslot >> 1; half > 0; half >>= 1) {
+            const int cell = (slot >= half ? slot - half : slot) * MT + rg;
+            float *mo = merge + cell * 16 * (C::MERGE_ROW + 2);
+            float *ml = mo + 16 * C::MERGE_ROW;
+            if (slot >= half && slot < 2 * half) {
+#pragma unroll
+                for (int i = 0; i < 2 * KS; ++i) {
+                    *reinterpret_cast<float2 *>(mo + gid * C::MERGE_ROW + i * 8 + tig * 2) = make_float2(o[i][0], o[i][1]);
+                    *reinterpret_cast<float2 *>(mo + (gid + 8) * C::MERGE_ROW + i * 8 + tig * 2) =
+                        make_float2(o[i][2], o[i][3]);
+                }
+                if (tig == 0)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) ml[(gid + 8 * r) * 2] = m[r], ml[(gid + 8 * r) * 2 + 1] = l[r];
+            }
+            named_bar_sync(1, CW * 32);
+            if (slot < half) {
+                float fa[2], fb[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float om = ml[(gid + 8 * r) * 2], ol = ml[(gid + 8 * r) * 2 + 1];
+                    const float nm = fmaxf(m[r], om), mu = nm == -INFINITY ? 0.f : nm;
+                    fa[r] = ex2_approx(m[r] - mu), fb[r] = ex2_approx(om - mu);
+                    l[r] = l[r] * fa[r] + ol * fb[r];
+                    m[r] = nm;
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * KS; ++i) {
+                    const float2 x = *reinterpret_cast<const float2 *>(mo + gid * C::MERGE_ROW + i * 8 + tig * 2);
+                    const float2 y = *reinterpret_cast<const float2 *>(mo + (gid + 8) * C::MERGE_ROW + i * 8 + tig * 2);
+                    o[i][0] = o[i][0] * fa[0] + x.x * fb[0], o[i][1] = o[i][1] * fa[0] + x.y * fb[0];
+                    o[i][2] = o[i][2] * fa[1] + y.x * fb[1], o[i][3] = o[i][3] * fa[1] + y.y * fb[1];
+                }
+            }
+            named_bar_sync(1, CW * 32);
+        }
+        if (slot == 0) {
+            const bool whole = g.whole();
+            const int64_t piece = (int64_t)blockIdx.x * 2 + g.slot();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (!have[r]) continue;
+                const int row = rbase + gid + 8 * r, tok = row / p.G, hg = row - tok * p.G;
+                const float inv = l[r] > 0.f ? p.v_inv / l[r] : 0.f;
+                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) : -INFINITY;
+                const int64_t orow = (int64_t)(g.s.q0 + tok) * p.H + g.h * p.G + hg;
+                const int trow = row - g.x.row0;
+                if (tig == 0) {
+                    if (!whole)
+                        p.part_l[piece * p.TM + trow] = ls;
+                    else if (p.lse)
+                        p.lse[orow] = ls * 0.6931471805599453f;
+                }
+                uint16_t *dst = static_cast<uint16_t *>(p.out) + orow * D;
+                float *prt = p.part_o + (piece * p.TM + trow) * D;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    const float a0 = o[2 * j][2 * r] * inv, a1 = o[2 * j][2 * r + 1] * inv;
+                    const float b0 = o[2 * j + 1][2 * r] * inv, b1 = o[2 * j + 1][2 * r + 1] * inv;
+                    if (E4M3) {  // four consecutive elements
+                        const int d = 16 * j + tig * 4;
+                        if (whole)
+                            *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack2<IO_F16>(a0, b0), pack2<IO_F16>(a1, b1));
+                        else
+                            *reinterpret_cast<float4 *>(prt + d) = make_float4(a0, b0, a1, b1);
+                    } else {
+                        const int d = 16 * j + tig * 2;
+                        if (whole) {
+                            *reinterpret_cast<uint32_t *>(dst + d) = pack2<IO_F16>(a0, a1);
+                            *reinterpret_cast<uint32_t *>(dst + d + 8) = pack2<IO_F16>(b0, b1);
+                        } else {
+                            *reinterpret_cast<float2 *>(prt + d) = make_float2(a0, a1);
+                            *reinterpret_cast<float2 *>(prt + d + 8) = make_float2(b0, b1);
+                        }
+                    }
+                }
+            }
+            if (g.slot() == 1 && !whole && rg == 0 && lane == 0)
+                p.rec[blockIdx.x] = PieceRec{1, g.b, g.h, g.t, cur.at - (g.u_end - g.u_begin) + g.x.nu, cur.total};
+        }
+    }
+}
+
+// Joins the pieces of the tile that began in CTA blockIdx.x and went on: row
+// by row, out = sum_i w_i o_i / sum_i w_i with w_i = 2^(lse_i - max lse), over
+// the pieces in the order of the line.  One warp a row.
+constexpr int JOIN_WARPS = 8;
+template <int D, bool IO_F16>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const PagedAttnParams p, int nc) {
+    pdl_wait();  // the pieces come from the previous kernel
+    const int c = blockIdx.x, lane = lane_id();
+    const PieceRec rec = p.rec[c];
+    if (!rec.valid) return;
+    const SeqInfo s = seq_info(p, rec.b);
+    const int row0 = rec.t * p.TM, rows = min(p.TM, s.n * p.G - row0);
+    const int r = blockIdx.y * JOIN_WARPS + warp_id();
+    if (r >= rows) return;
+    int last = c + 1;  // pieces: slot 1 of c, slot 0 of c + 1 .. last - 1
+    while (last < nc && line_start(rec.total, last, nc) < rec.end) ++last;
+    auto at = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.TM + r; };
+    float mx = -INFINITY;
+    for (int i = c; i < last; ++i)
+        if (i == c || line_start(rec.total, i, nc) < line_start(rec.total, i + 1, nc)) mx = fmaxf(mx, p.part_l[at(i)]);
+    constexpr int V = D / 32;
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    if (mx != -INFINITY) {
+        for (int i = c; i < last; ++i) {
+            if (i != c && line_start(rec.total, i, nc) >= line_start(rec.total, i + 1, nc)) continue;
+            const float w = ex2_approx(p.part_l[at(i)] - mx);
+            const float *o = p.part_o + at(i) * D + lane * V;
+            sum += w;
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = fmaf(w, o[j], acc[j]);
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int row = row0 + r, tok = row / p.G;
+    const int64_t orow = (int64_t)(s.q0 + tok) * p.H + rec.h * p.G + (row - tok * p.G);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow * D + lane * V);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) dst[j / 2] = pack2<IO_F16>(acc[j] * inv, acc[j + 1] * inv);
+    if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Rows of a tile: enough 16-row groups for one sequence's packed rows, up to 128.
+int tile_groups(int64_t max_rows) {
+    int mt = 1;
+    while (mt < CW && mt * 16 < max_rows) mt *= 2;
+    return mt;
+}
+
+struct Plan {
+    int MT, nc;
+    size_t o_off, l_off, rec_off, total;
+};
+Plan make_plan(int num_seqs, int H, int Hkv, int D, int max_q, int max_len, int window, int sms) {
+    Plan pl{};
+    const int64_t rows = (int64_t)max_q * (H / Hkv);
+    pl.MT = tile_groups(rows);
+    const int TM = pl.MT * 16;
+    const int64_t tiles = (rows + TM - 1) / TM;
+    int64_t units = (max_len + UNIT - 1) / UNIT;
+    if (window) {
+        const int64_t w = ((int64_t)window + TM) / UNIT + 2;
+        units = w < units ? w : units;
+    }
+    int64_t most = units;  // no more CTAs than units in the largest call of these bounds
+    for (const int64_t x : {tiles, (int64_t)Hkv, (int64_t)num_seqs}) most = most > sms ? most : most * x;
+    pl.nc = (int)(most < sms ? most : sms);
+    size_t off = 0;
+    pl.o_off = off, off += align_up((size_t)pl.nc * 2 * TM * D * 4, 256);
+    pl.l_off = off, off += align_up((size_t)pl.nc * 2 * TM * 4, 256);
+    pl.rec_off = off, off += align_up((size_t)pl.nc * sizeof(PieceRec), 256);
+    pl.total = off;
+    return pl;
+}
+
+bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int pages, int64_t page, int64_t row,
+            int64_t head) {
+    const int e = dtype == DSA_E4M3 ? 1 : 2;
+    const int inner = D * e < 128 ? D : 128 / e;
+    const uint64_t dims[4] = {(uint64_t)D, 64, (uint64_t)heads, (uint64_t)pages};
+    // the stride of a dimension of one entry only has to be a valid one
+    const uint64_t strides[3] = {(uint64_t)(row * e), (uint64_t)((heads > 1 ? head : row) * e),
+                                 (uint64_t)((pages > 1 ? page : row) * e)};
+    const uint32_t box[4] = {(uint32_t)inner, UNIT, 1, 1};
+    const CUtensorMapDataType dt = dtype == DSA_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : dtype == DSA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return make_tmap_4d(m, base, dt, dims, strides, box,
+                        inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int D, bool IO_F16, bool E4M3>
+dsa_status launch(const CUtensorMap &km, const CUtensorMap &vm, const PagedAttnParams &p, const Plan &pl,
+                  cudaStream_t st) {
+    auto fn = paged_attn_kernel<D, IO_F16, E4M3>;
+    constexpr int SMEM = Cfg<D, E4M3>::SMEM;
+    if (!ensure_smem(reinterpret_cast<const void *>(fn), SMEM)) return DSA_ERR_CUDA;
+    fn<<<pl.nc, THREADS, SMEM, st>>>(km, vm, p, pl.MT);
+    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+    if (pl.nc == 1) return DSA_OK;  // one CTA holds every tile whole
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(pl.nc - 1, (p.TM + JOIN_WARPS - 1) / JOIN_WARPS);
+    cfg.blockDim = dim3(JOIN_WARPS * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, IO_F16>, p, pl.nc) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, int32_t cache_dtype,
+                                  int32_t max_q, int32_t max_len, int32_t window, int sm_count) {
+    return make_plan(num_seqs, H, Hkv, D, max_q, max_len, window, sm_count).total;
+}
+
+dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
+    const DeviceInfo *dev = current_device();
+    if (!dev) return DSA_ERR_CUDA;
+    const dsa_kv_cache &c = *a.cache;
+    const int H = a.q.heads, D = c.Dk;
+    const Plan pl = make_plan(a.pg.num_seqs, H, c.heads, D, a.max_q, a.max_len, a.window, dev->sm_count);
+    if (!a.ws || a.ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(a.ws) & 255u)) return DSA_ERR_WORKSPACE;
+    CUtensorMap km, vm;
+    if (!kv_map(&km, c.k, c.dtype, D, c.heads, a.pg.num_pages, c.k_page_stride, c.k_row_stride, c.k_head_stride) ||
+        !kv_map(&vm, c.v, c.dtype, D, c.heads, a.pg.num_pages, c.v_page_stride, c.v_row_stride, c.v_head_stride))
+        return DSA_ERR_CUDA;
+    const bool e4m3 = c.dtype == DSA_E4M3;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    PagedAttnParams p{};
+    p.q = a.q.data, p.q_token = a.q.token_stride, p.q_head = a.q.head_stride;
+    p.q_start = a.q_start, p.pg = a.pg;
+    p.T = a.T, p.H = H, p.Hkv = c.heads, p.G = H / c.heads, p.TM = pl.MT * 16;
+    p.max_q = a.max_q, p.max_len = a.max_len, p.window = a.window;
+    p.scale_log2 = (float)(a.sm_scale * 1.4426950408889634 / (e4m3 ? c.k_scale : 1.f));
+    p.v_inv = e4m3 ? 1.f / c.v_scale : 1.f;
+    p.out = a.out, p.lse = a.lse;
+    p.part_o = reinterpret_cast<float *>(ws + pl.o_off);
+    p.part_l = reinterpret_cast<float *>(ws + pl.l_off);
+    p.rec = reinterpret_cast<PieceRec *>(ws + pl.rec_off);
+    p.err = dev->err;
+    const bool f16 = a.dtype == DSA_F16;
+#define DSA_PAGED(D_)                                                                     \
+    (f16 ? (e4m3 ? launch<D_, true, true>(km, vm, p, pl, st) : launch<D_, true, false>(km, vm, p, pl, st)) \
+         : (e4m3 ? launch<D_, false, true>(km, vm, p, pl, st) : launch<D_, false, false>(km, vm, p, pl, st)))
+    return D == 128 ? DSA_PAGED(128) : DSA_PAGED(64);
+#undef DSA_PAGED
+}
+
+}  // namespace dsa

@@ -1,0 +1,245 @@
+// Sharing the work of dsa_paged_attn out over CTAs.
+//
+// A tile is TM packed rows of one sequence and one K/V head: row r is query
+// head (r % G) of the group and the sequence's new token r / G, so all query
+// heads that share a K/V head share its loads.  Its work is the run of units
+// (UNIT consecutive key positions, aligned) that its rows see.  All tiles'
+// units, in the order sequence, head, tile, unit, form one line, which is cut
+// into equal parts, one per CTA: whatever the mix of lengths, every CTA gets
+// the same number of units, and a long sequence of few heads is split over as
+// many CTAs as it takes.  A CTA that holds a tile whole writes its rows;
+// pieces of a tile go to the workspace (at most two per CTA: one that began
+// in an earlier CTA, one that goes on in the next) and are joined by a second
+// kernel in the order of the line.  Lengths are read on the device: every CTA
+// sums the units itself (a few thousand instructions at most), and its result
+// depends on nothing but the lengths.
+#pragma once
+
+#include "dsa_device.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+
+struct PagedAttnParams {
+    const void *q;
+    int64_t q_token, q_head;
+    const int32_t *q_start;
+    PagedDev pg;
+    int32_t T, H, Hkv, G, TM;
+    int32_t max_q, max_len, window;
+    float scale_log2;  // sm_scale * log2(e) (and 1 / k_scale)
+    float v_inv;       // 1 / v_scale
+    void *out;
+    float *lse;
+    float *part_o;   // [CTAs][2][TM][D]: normalised partial outputs
+    float *part_l;   // [CTAs][2][TM]: log2 of the sum of exponentials
+    struct PieceRec *rec;  // [CTAs]
+    uint32_t *err;
+};
+
+// A tile that began in this CTA and goes on in the next ones.
+struct PieceRec {
+    int32_t valid, b, h, t;
+    int64_t end, total;  // where the tile's units end on the line; the line's length
+};
+
+struct SeqInfo {
+    int n, L, q0;  // new tokens, length, first row of q
+};
+__device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams &p, int b, bool report = false) {
+    SeqInfo s;
+    s.L = max(p.pg.seq_lens[b], 0);
+    uint32_t bad = 0;
+    if (p.q_start) {
+        s.q0 = p.q_start[b];
+        const int64_t n = (int64_t)p.q_start[b + 1] - s.q0;
+        if (s.q0 < 0 || n < 0 || s.q0 + n > p.T || n > p.max_q) bad = DSA_DEVERR_SHAPE;
+        s.n = (int)n;
+    } else {
+        s.q0 = b;
+        s.n = 1;
+    }
+    if (s.L > p.max_len) bad = DSA_DEVERR_SHAPE;
+    if (bad) {
+        if (report) record_error(p.err, bad);
+        s.n = 0;
+    }
+    return s;
+}
+
+struct Tile {
+    int row0, rows;        // packed rows
+    int p_first, p_last;   // positions of its first and last token (below 0: no such position)
+    int key_lo, key_hi;    // positions that some row sees
+    int u0, nu;            // units
+};
+template <int UNIT>
+__device__ __forceinline__ Tile tile_info(const PagedAttnParams &p, const SeqInfo &s, int t) {
+    Tile x;
+    const int total = s.n * p.G;
+    x.row0 = t * p.TM;
+    x.rows = min(p.TM, total - x.row0);
+    x.p_first = s.L - s.n + x.row0 / p.G;
+    x.p_last = s.L - s.n + (x.row0 + x.rows - 1) / p.G;
+    x.key_hi = max(x.p_last + 1, 0);
+    x.key_lo = p.window ? max(x.p_first - p.window + 1, 0) : 0;
+    x.u0 = x.key_lo / UNIT;
+    x.nu = max((x.key_hi + UNIT - 1) / UNIT - x.u0, 1);  // a tile that sees nothing has one unit, for its zeros
+    return x;
+}
+__device__ __forceinline__ int seq_tiles(const PagedAttnParams &p, const SeqInfo &s) {
+    return (int)(((int64_t)s.n * p.G + p.TM - 1) / p.TM);
+}
+
+// Where on the line CTA c of nc begins.
+__device__ __forceinline__ int64_t line_start(int64_t total, int c, int nc) { return total * c / nc; }
+
+struct Cursor {
+    int b, h, t, u;   // sequence, K/V head, tile, unit of the tile
+    int64_t at, end;  // this place on the line, and the CTA's end
+    int64_t total;
+};
+
+constexpr int PLAN_SEQS = 1024;
+struct PlanShared {
+    int64_t units[PLAN_SEQS];  // per sequence, one head
+    int64_t total;
+    Cursor cur;
+    int found;
+};
+
+// All threads of the block; the result is in sh.cur for all of them.
+template <int UNIT>
+__device__ void plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh) {
+    const int lane = lane_id(), warp = warp_id(), nw = blockDim.x >> 5;
+    const int B = p.pg.num_seqs;
+    const bool single = (int64_t)p.max_q * p.G <= p.TM;  // one tile a sequence at most
+    auto fill = [&](int base, bool report) {
+        const int cnt = min(PLAN_SEQS, B - base);
+        if (single) {
+            for (int i = threadIdx.x; i < cnt; i += blockDim.x) {
+                const SeqInfo s = seq_info(p, base + i, report);
+                sh.units[i] = s.n ? tile_info<UNIT>(p, s, 0).nu : 0;
+            }
+        } else {
+            for (int i = warp; i < cnt; i += nw) {
+                const SeqInfo s = seq_info(p, base + i, report && lane == 0);
+                const int nt = seq_tiles(p, s);
+                int64_t sum = 0;
+                for (int t = lane; t < nt; t += 32) sum += tile_info<UNIT>(p, s, t).nu;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) sh.units[i] = sum;
+            }
+        }
+        __syncthreads();
+        return cnt;
+    };
+    if (threadIdx.x == 0) sh.total = 0, sh.found = 0;
+    for (int base = 0; base < B; base += PLAN_SEQS) {
+        const int cnt = fill(base, c == 0);
+        if (warp == 0) {
+            int64_t sum = 0;
+            for (int i = lane; i < cnt; i += 32) sum += sh.units[i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) sh.total += sum * p.Hkv;
+        }
+        __syncthreads();
+    }
+    const int64_t total = sh.total;
+    const int64_t begin = line_start(total, c, nc), end = line_start(total, c + 1, nc);
+    if (threadIdx.x == 0) sh.cur = Cursor{0, 0, 0, 0, begin, end, total};
+    __syncthreads();
+    if (begin >= end) return;
+    int64_t before = 0;  // warp 0: units before the group of 32 sequences looked at
+    for (int base = 0; base < B; base += PLAN_SEQS) {
+        const int cnt = B > PLAN_SEQS ? fill(base, false) : B;
+        if (warp == 0) {
+            for (int g = 0; g < cnt; g += 32) {
+                const int64_t w = g + lane < cnt ? sh.units[g + lane] * p.Hkv : 0;
+                int64_t inc = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += v;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, before + inc > begin);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    const int b = base + g + l;
+                    const int64_t per_head = sh.units[g + l];
+                    int64_t off = begin - before - __shfl_sync(0xffffffffu, inc - w, l);
+                    const int h = (int)(off / per_head);
+                    off -= h * per_head;
+                    const SeqInfo s = seq_info(p, b);
+                    const int nt = seq_tiles(p, s);
+                    int64_t sum = 0;
+                    for (int t0 = 0; t0 < nt; t0 += 32) {
+                        const int64_t nu = t0 + lane < nt ? tile_info<UNIT>(p, s, t0 + lane).nu : 0;
+                        int64_t ti = nu;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int64_t v = __shfl_up_sync(0xffffffffu, ti, o);
+                            if (lane >= o) ti += v;
+                        }
+                        const uint32_t tp = __ballot_sync(0xffffffffu, sum + ti > off);
+                        if (tp) {
+                            const int tl = __ffs(tp) - 1;
+                            if (lane == tl) {
+                                sh.cur.b = b, sh.cur.h = h, sh.cur.t = t0 + tl;
+                                sh.cur.u = (int)(off - sum - (ti - nu));
+                                sh.found = 1;
+                            }
+                            break;
+                        }
+                        sum += __shfl_sync(0xffffffffu, ti, 31);
+                    }
+                    break;
+                }
+                before += __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+        __syncthreads();
+        if (sh.found) break;
+    }
+    __syncthreads();
+}
+
+// A run of units of one tile that a CTA works on.
+struct Segment {
+    SeqInfo s;
+    Tile x;
+    int b, h, t;
+    int u_begin, u_end;  // of the tile's units
+    __device__ __forceinline__ bool whole() const { return u_begin == 0 && u_end == x.nu; }
+    __device__ __forceinline__ int slot() const { return u_begin == 0 ? 1 : 0; }  // of the CTA's two pieces
+};
+// The next segment, or false at the CTA's end.  Every role of a CTA walks the
+// same segments with its own copy of the cursor.
+template <int UNIT>
+__device__ __forceinline__ bool next_segment(const PagedAttnParams &p, Cursor &c, Segment &g) {
+    if (c.at >= c.end) return false;
+    g.s = seq_info(p, c.b);
+    int nt = seq_tiles(p, g.s);
+    while (c.t >= nt) {  // the cursor stands behind a head's last tile, or at a sequence without rows
+        c.t = 0;
+        if (nt == 0 || ++c.h == p.Hkv) {
+            c.h = 0;
+            if (++c.b >= p.pg.num_seqs) return false;  // the lengths changed under the call
+            g.s = seq_info(p, c.b);
+            nt = seq_tiles(p, g.s);
+        }
+    }
+    g.x = tile_info<UNIT>(p, g.s, c.t);
+    g.b = c.b, g.h = c.h, g.t = c.t;
+    g.u_begin = c.u;
+    const int64_t left = c.end - c.at;
+    g.u_end = left < g.x.nu - c.u ? c.u + (int)left : g.x.nu;
+    c.at += g.u_end - g.u_begin;
+    c.u = 0;
+    ++c.t;
+    return true;
+}
+
+}  // namespace dsa
