@@ -19,7 +19,7 @@
 
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
-#include "paged_plan.cuh"
+#include "paged_attn.cuh"
 
 namespace dsa {
 namespace {
@@ -81,15 +81,6 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b
 }
 
 template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if (F16) {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
     if (F16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
@@ -99,15 +90,6 @@ __device__ __forceinline__ uint32_t widen(uint32_t v) {
     uint32_t r;
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(v));
     return r;
-}
-
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
-                                            int32_t z, int32_t w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-        : "memory");
 }
 
 // MT = TM / 16 row groups of 16; the consumer warps are MT row groups x CW/MT
@@ -245,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const float2 a = unpack2<false>(qf[k][r + 2 * x]);
-                            qf[k][r + 2 * x] = pack2<true>(a.x * down, a.y * down);
+                            qf[k][r + 2 * x] = paged_pack2<true>(a.x * down, a.y * down);
                         }
                     }
                 }
@@ -318,8 +300,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 2 * KS; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
             }
             // weights rounded to the values' type for the second product (their sum l is of the unrounded ones)
-            const uint32_t a[4] = {pack2<MM_F16>(s[0][0], s[0][1]), pack2<MM_F16>(s[0][2], s[0][3]),
-                                   pack2<MM_F16>(s[1][0], s[1][1]), pack2<MM_F16>(s[1][2], s[1][3])};
+            const uint32_t a[4] = {paged_pack2<MM_F16>(s[0][0], s[0][1]), paged_pack2<MM_F16>(s[0][2], s[0][3]),
+                                   paged_pack2<MM_F16>(s[1][0], s[1][1]), paged_pack2<MM_F16>(s[1][2], s[1][3])};
             // values at positions that no row of the tile sees may be anything (unwritten rows): taken as 0
             uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
             const bool clear = key0 + 16 > g.x.key_hi || key0 < g.x.key_lo;
@@ -442,14 +424,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (E4M3) {  // four consecutive elements
                         const int d = 16 * j + tig * 4;
                         if (whole)
-                            *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack2<IO_F16>(a0, b0), pack2<IO_F16>(a1, b1));
+                            *reinterpret_cast<uint2 *>(dst + d) = make_uint2(paged_pack2<IO_F16>(a0, b0), paged_pack2<IO_F16>(a1, b1));
                         else
                             *reinterpret_cast<float4 *>(prt + d) = make_float4(a0, b0, a1, b1);
                     } else {
                         const int d = 16 * j + tig * 2;
                         if (whole) {
-                            *reinterpret_cast<uint32_t *>(dst + d) = pack2<IO_F16>(a0, a1);
-                            *reinterpret_cast<uint32_t *>(dst + d + 8) = pack2<IO_F16>(b0, b1);
+                            *reinterpret_cast<uint32_t *>(dst + d) = paged_pack2<IO_F16>(a0, a1);
+                            *reinterpret_cast<uint32_t *>(dst + d + 8) = paged_pack2<IO_F16>(b0, b1);
                         } else {
                             *reinterpret_cast<float2 *>(prt + d) = make_float2(a0, a1);
                             *reinterpret_cast<float2 *>(prt + d + 8) = make_float2(b0, b1);
@@ -502,7 +484,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
     const int64_t orow = (int64_t)(s.q0 + tok) * p.H + rec.h * p.G + (row - tok * p.G);
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow * D + lane * V);
 #pragma unroll
-    for (int j = 0; j < V; j += 2) dst[j / 2] = pack2<IO_F16>(acc[j] * inv, acc[j + 1] * inv);
+    for (int j = 0; j < V; j += 2) dst[j / 2] = paged_pack2<IO_F16>(acc[j] * inv, acc[j + 1] * inv);
     if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -514,18 +496,17 @@ int tile_groups(int64_t max_rows) {
 }
 
 struct Plan {
-    int MT, nc;
+    int TM, nc;
     size_t o_off, l_off, rec_off, total;
 };
-Plan make_plan(int num_seqs, int H, int Hkv, int D, int max_q, int max_len, int window, int sms) {
+// `unit` keys a unit, tiles of TM rows.
+Plan make_plan(int TM, int unit, int num_seqs, int G, int Hkv, int D, int max_q, int max_len, int window, int sms) {
     Plan pl{};
-    const int64_t rows = (int64_t)max_q * (H / Hkv);
-    pl.MT = tile_groups(rows);
-    const int TM = pl.MT * 16;
-    const int64_t tiles = (rows + TM - 1) / TM;
-    int64_t units = (max_len + UNIT - 1) / UNIT;
+    pl.TM = TM;
+    const int64_t tiles = ((int64_t)max_q * G + TM - 1) / TM;
+    int64_t units = ((int64_t)max_len + unit - 1) / unit;
     if (window) {
-        const int64_t w = ((int64_t)window + TM) / UNIT + 2;
+        const int64_t w = ((int64_t)window + TM) / unit + 2;
         units = w < units ? w : units;
     }
     int64_t most = units;  // no more CTAs than units in the largest call of these bounds
@@ -539,6 +520,19 @@ Plan make_plan(int num_seqs, int H, int Hkv, int D, int max_q, int max_len, int 
     return pl;
 }
 
+// Chunks go to the tensor-core kernel: more packed rows a K/V head than the
+// warp-level kernel's widest tile but one, so that at least a quarter of the
+// 256-row tile is real.
+bool tc_shape(int G, int max_q, int cache_dtype) {
+    return cache_dtype != DSA_E4M3 && G <= 128 && (int64_t)max_q * G > 64;
+}
+// What else the tensor-core kernel needs of a call: a positive scale (the
+// maximum is taken before scaling) and q reachable by a tensor map.
+bool tc_call(const PagedAttnArgs &a) {
+    auto ok = [](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < ((int64_t)1 << 39)); };
+    return a.sm_scale > 0 && ok(a.q.token_stride, a.T) && ok(a.q.head_stride, a.q.heads);
+}
+
 bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int pages, int64_t page, int64_t row,
             int64_t head) {
     const int e = dtype == DSA_E4M3 ? 1 : 2;
@@ -547,7 +541,7 @@ bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int p
     // the stride of a dimension of one entry only has to be a valid one
     const uint64_t strides[3] = {(uint64_t)(row * e), (uint64_t)((heads > 1 ? head : row) * e),
                                  (uint64_t)((pages > 1 ? page : row) * e)};
-    const uint32_t box[4] = {(uint32_t)inner, UNIT, 1, 1};
+    const uint32_t box[4] = {(uint32_t)inner, 64, 1, 1};
     const CUtensorMapDataType dt = dtype == DSA_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : dtype == DSA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -556,49 +550,65 @@ bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int p
 }
 
 template <int D, bool IO_F16, bool E4M3>
-dsa_status launch(const CUtensorMap &km, const CUtensorMap &vm, const PagedAttnParams &p, const Plan &pl,
-                  cudaStream_t st) {
+dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
     auto fn = paged_attn_kernel<D, IO_F16, E4M3>;
     constexpr int SMEM = Cfg<D, E4M3>::SMEM;
     if (!ensure_smem(reinterpret_cast<const void *>(fn), SMEM)) return DSA_ERR_CUDA;
-    fn<<<pl.nc, THREADS, SMEM, st>>>(km, vm, p, pl.MT);
-    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-    if (pl.nc == 1) return DSA_OK;  // one CTA holds every tile whole
+    CUtensorMap km, vm;
+    if (!paged_kv_maps(*a.cache, a.pg.num_pages, &km, &vm)) return DSA_ERR_CUDA;
+    fn<<<nc, THREADS, SMEM, st>>>(km, vm, p, p.TM / 16);
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+template <int D, bool IO_F16>
+dsa_status launch_join(const PagedAttnParams &p, int nc, cudaStream_t st) {
+    if (nc == 1) return DSA_OK;  // one CTA holds every tile whole
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(pl.nc - 1, (p.TM + JOIN_WARPS - 1) / JOIN_WARPS);
+    cfg.gridDim = dim3(nc - 1, (p.TM + JOIN_WARPS - 1) / JOIN_WARPS);
     cfg.blockDim = dim3(JOIN_WARPS * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at, cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, IO_F16>, p, pl.nc) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, IO_F16>, p, nc) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace
 
+bool paged_kv_maps(const dsa_kv_cache &c, int num_pages, CUtensorMap *km, CUtensorMap *vm) {
+    return kv_map(km, c.k, c.dtype, c.Dk, c.heads, num_pages, c.k_page_stride, c.k_row_stride, c.k_head_stride) &&
+           kv_map(vm, c.v, c.dtype, c.Dk, c.heads, num_pages, c.v_page_stride, c.v_row_stride, c.v_head_stride);
+}
+
 size_t paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, int32_t cache_dtype,
                                   int32_t max_q, int32_t max_len, int32_t window, int sm_count) {
-    return make_plan(num_seqs, H, Hkv, D, max_q, max_len, window, sm_count).total;
+    const int G = H / Hkv;
+    size_t need = make_plan(16 * tile_groups((int64_t)max_q * G), UNIT, num_seqs, G, Hkv, D, max_q, max_len, window,
+                            sm_count).total;
+    if (tc_shape(G, max_q, cache_dtype)) {  // (the call's scale and strides decide between the two)
+        const size_t tc =
+            make_plan(paged_attn_tc_rows(G), 128, num_seqs, G, Hkv, D, max_q, max_len, window, sm_count).total;
+        need = tc > need ? tc : need;
+    }
+    return need;
 }
 
 dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     const DeviceInfo *dev = current_device();
     if (!dev) return DSA_ERR_CUDA;
     const dsa_kv_cache &c = *a.cache;
-    const int H = a.q.heads, D = c.Dk;
-    const Plan pl = make_plan(a.pg.num_seqs, H, c.heads, D, a.max_q, a.max_len, a.window, dev->sm_count);
+    const int H = a.q.heads, D = c.Dk, G = H / c.heads;
+    const bool tc = tc_shape(G, a.max_q, c.dtype) && tc_call(a);
+    const Plan pl = make_plan(tc ? paged_attn_tc_rows(G) : 16 * tile_groups((int64_t)a.max_q * G), tc ? 128 : UNIT,
+                              a.pg.num_seqs, G, c.heads, D, a.max_q, a.max_len, a.window, dev->sm_count);
     if (!a.ws || a.ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(a.ws) & 255u)) return DSA_ERR_WORKSPACE;
-    CUtensorMap km, vm;
-    if (!kv_map(&km, c.k, c.dtype, D, c.heads, a.pg.num_pages, c.k_page_stride, c.k_row_stride, c.k_head_stride) ||
-        !kv_map(&vm, c.v, c.dtype, D, c.heads, a.pg.num_pages, c.v_page_stride, c.v_row_stride, c.v_head_stride))
-        return DSA_ERR_CUDA;
     const bool e4m3 = c.dtype == DSA_E4M3;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     PagedAttnParams p{};
     p.q = a.q.data, p.q_token = a.q.token_stride, p.q_head = a.q.head_stride;
     p.q_start = a.q_start, p.pg = a.pg;
-    p.T = a.T, p.H = H, p.Hkv = c.heads, p.G = H / c.heads, p.TM = pl.MT * 16;
+    p.T = a.T, p.H = H, p.Hkv = c.heads, p.G = G, p.TM = pl.TM;
     p.max_q = a.max_q, p.max_len = a.max_len, p.window = a.window;
     p.scale_log2 = (float)(a.sm_scale * 1.4426950408889634 / (e4m3 ? c.k_scale : 1.f));
     p.v_inv = e4m3 ? 1.f / c.v_scale : 1.f;
@@ -608,11 +618,16 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     p.rec = reinterpret_cast<PieceRec *>(ws + pl.rec_off);
     p.err = dev->err;
     const bool f16 = a.dtype == DSA_F16;
-#define DSA_PAGED(D_)                                                                     \
-    (f16 ? (e4m3 ? launch<D_, true, true>(km, vm, p, pl, st) : launch<D_, true, false>(km, vm, p, pl, st)) \
-         : (e4m3 ? launch<D_, false, true>(km, vm, p, pl, st) : launch<D_, false, false>(km, vm, p, pl, st)))
-    return D == 128 ? DSA_PAGED(128) : DSA_PAGED(64);
+    dsa_status s;
+#define DSA_PAGED(D_)                                                                        (f16 ? (e4m3 ? launch<D_, true, true>(a, p, pl.nc, st) : launch<D_, true, false>(a, p, pl.nc, st))          : (e4m3 ? launch<D_, false, true>(a, p, pl.nc, st) : launch<D_, false, false>(a, p, pl.nc, st)))
+    if (tc)
+        s = launch_paged_attn_tc(a, p, pl.nc, st);
+    else
+        s = D == 128 ? DSA_PAGED(128) : DSA_PAGED(64);
 #undef DSA_PAGED
+    if (s != DSA_OK) return s;
+    if (D == 128) return f16 ? launch_join<128, true>(p, pl.nc, st) : launch_join<128, false>(p, pl.nc, st);
+    return f16 ? launch_join<64, true>(p, pl.nc, st) : launch_join<64, false>(p, pl.nc, st);
 }
 
 }  // namespace dsa

@@ -1,0 +1,494 @@
+// Attention of chunks of new tokens over the paged K/V cache: the same sums
+// as paged_attn.cu on the fifth-generation tensor cores, for many packed rows
+// a K/V head.  Tensor-bound: 4 D flops for each (query, head, key).
+//
+// One CTA per SM takes tiles of two row blocks ("streams") of up to 128
+// packed rows (whole tokens: 128 / G of them) against units of 128 keys (two
+// pages) that both streams share.  Per unit and stream: S = Q K^T into 128
+// tensor-memory columns; a warpgroup turns S into the weights P (its thread r
+// holds row r: no exchange between threads) and writes them over S; O += P V
+// with P read from tensor memory and V, as it lies in the cache, as the
+// N-major operand.  The streams run half a step apart, so that one's products
+// fill the time of the other's exponentials:
+//
+//   tensor pipe:  ... PV0(i-1) S0(i) PV1(i-1) S1(i) PV0(i) S0(i+1) ...
+//   warps 0-3:                      [softmax 0 (i)]
+//   warps 4-7:        [softmax 1 (i-1)]            [softmax 1 (i)]
+//
+// Tensor memory is full: S0 S1 O0 O1 at 128 columns each.  The running
+// maximum that the weights refer to is only moved when it has grown by more
+// than 2^8 (weights stay below 2^8, their sum is fp32, and the quotient does
+// not depend on the reference), so O is rarely rescaled.  The 16-per-clock
+// exponential unit would take as long as the two matrix products (2048 clocks
+// a unit at D = 128); a part of the exponentials goes to a degree-4 polynomial
+// on the FMA pipe instead.
+#include <cuda_fp16.h>
+
+#include "dsa_device.cuh"
+#include "dsa_internal.h"
+#include "paged_attn.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int UNIT = 128;
+constexpr int THREADS = 384;  // two softmax warpgroups, one of single-warp roles
+constexpr int MMA_WARP = 8, LOAD_WARP = 9;
+// registers: 384 x 168 at launch; the roles' shares add up to the same
+constexpr int REG_LAUNCH = 168, REG_SOFTMAX = 208, REG_REST = 88;
+static_assert(256 * REG_SOFTMAX + 128 * REG_REST == THREADS * REG_LAUNCH, "register shares");
+
+template <int D>
+struct Cfg {
+    static constexpr int NH = D / 64;                 // 128-byte column blocks of a row
+    static constexpr int BLOCK = 128 * 128;           // [128 rows][64 elements]
+    static constexpr int TILE = NH * BLOCK;           // Q of a stream, K or V of a unit
+    static constexpr int NST = 160 * 1024 / TILE;     // ring slots (K and V alternate)
+    static constexpr int SMEM = 2 * TILE + NST * TILE + 1024;
+    static constexpr uint32_t O_COL = 256;            // S0 at 0, S1 at 128, O0, O1
+};
+
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+
+// Two fp32 values in one 64-bit register pair.
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 upk(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^x for two finite x <= 16: x = n + f with n the nearest integer (adding 1.5 x 2^23 leaves it in the
+// low bits), 2^f on [-1/2, 1/2] by the degree-4 polynomial of least relative error (2.7e-6 in fp32,
+// computed by exchange on that interval), n added to the exponent.  Below 2^-126: 2^-126.
+__device__ __forceinline__ float2 ex2_poly(uint64_t x2) {
+    float2 x = upk(x2);
+    x.x = fmaxf(x.x, -126.f), x.y = fmaxf(x.y, -126.f);
+    const uint64_t xc = pk(x.x, x.y);
+    const uint64_t t = add2(xc, pk(12582912.f, 12582912.f));
+    const uint64_t n = add2(t, pk(-12582912.f, -12582912.f));
+    const uint64_t f = fma2(n, pk(-1.f, -1.f), xc);
+    uint64_t p = fma2(pk(0.009570102207362652f, 0.009570102207362652f), f, pk(0.05591785907745361f, 0.05591785907745361f));
+    p = fma2(p, f, pk(0.240247443318367f, 0.240247443318367f));
+    p = fma2(p, f, pk(0.6931217908859253f, 0.6931217908859253f));
+    p = fma2(p, f, pk(0.9999992847442627f, 0.9999992847442627f));
+    const float2 pf = upk(p), tf = upk(t);
+    return make_float2(__uint_as_float(__float_as_uint(pf.x) + (__float_as_uint(tf.x) << 23)),
+                       __uint_as_float(__float_as_uint(pf.y) + (__float_as_uint(tf.y) << 23)));
+}
+
+// A stream's rows of a tile, and the segment's units that they see ([lo, hi), of the tile's units).
+struct Stream {
+    int rows, lo, hi;
+    int p_first, p_last, key_lo, key_hi;
+};
+__device__ __forceinline__ Stream stream_info(const PagedAttnParams &p, const Segment &g, int st) {
+    Stream s;
+    const int rs = p.TM / 2, r0 = g.x.row0 + st * rs;
+    s.rows = min(max(g.x.rows - st * rs, 0), rs);
+    s.lo = s.hi = g.u_begin;
+    s.p_first = g.s.L - g.s.n + r0 / p.G;
+    s.p_last = s.p_first + s.rows / p.G - 1;  // rows are whole tokens
+    s.key_hi = max(s.p_last + 1, 0);
+    s.key_lo = p.window ? max(s.p_first - p.window + 1, 0) : 0;
+    if (s.rows > 0 && s.key_hi > s.key_lo) {
+        s.lo = max(s.key_lo / UNIT - g.x.u0, g.u_begin);
+        s.hi = max(min((s.key_hi + UNIT - 1) / UNIT - g.x.u0, g.u_end), s.lo);
+    }
+    return s;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const PagedAttnParams p) {
+    using C = Cfg<D>;
+    constexpr int NST = C::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *Qs = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = Qs + 2 * C::TILE;
+    __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const int warp = warp_id(), lane = lane_id();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
+            mbar_init(&s_full[s], 1), mbar_init(&p_full[s], 4), mbar_init(&o_full[s], 1);
+        }
+        mbar_init(&drain, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
+        p.rec[blockIdx.x].valid = 0;
+    }
+    if (warp == MMA_WARP) tmem_alloc(&tmem_slot, 512);
+    pdl_trigger();
+    PlanShared &plan = *reinterpret_cast<PlanShared *>(ring);  // before the ring's first use
+    plan_cta<UNIT>(p, blockIdx.x, gridDim.x, plan);
+    Cursor cur = plan.cur;
+    fence_proxy_async_smem();  // the plan's stores before the copies into the same memory
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Segment g;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
+        if (warp == LOAD_WARP) {
+            // ---- producer ----
+            uint32_t it = 0, qn[2] = {0, 0};  // ring slots used, loads of each stream's Q
+            bool ok = true;
+            auto slot_wait = [&](uint32_t i) {
+                if (ok && i >= NST) ok = mbar_wait(&empty[i % NST], ((i / NST) - 1) & 1, p.err, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto load_tile = [&](const CUtensorMap *map, int h, int pg0, int pg1) {  // one K or V tile
+                slot_wait(it);
+                if (!ok) return;
+                if (lane == 0) {
+                    uint64_t *bar = &full[it % NST];
+                    uint8_t *dst = ring + (it % NST) * C::TILE;
+                    mbar_expect_tx(bar, C::TILE);
+#pragma unroll
+                    for (int x = 0; x < C::NH; ++x) {
+                        tma_load_4d(dst + x * C::BLOCK, map, bar, x * 64, 0, h, pg0);
+                        tma_load_4d(dst + x * C::BLOCK + C::BLOCK / 2, map, bar, x * 64, 0, h, pg1);
+                    }
+                }
+                __syncwarp();
+                ++it;
+            };
+            while (ok && next_segment<UNIT>(p, cur, g)) {
+                const int hi_page = (g.x.key_hi + 63) / 64;
+                for (int u = g.u_begin; ok && u < g.u_end; u += 16) {
+                    int page = p.pg.num_pages;  // outside the map: reads as zeros
+                    const int lp = (g.x.u0 + u) * 2 + lane;
+                    // (the first unit's first page may lie before the window: not looked at)
+                    if (u + lane / 2 < g.u_end && lp < hi_page && lp >= g.x.key_lo / 64) {
+                        const int id = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)g.b * p.pg.max_blocks + lp] : -1;
+                        if (id >= 0 && id < p.pg.num_pages)
+                            page = id;
+                        else
+                            record_error(p.err, DSA_DEVERR_PAGE);
+                    }
+                    const int cnt = min(16, g.u_end - u);
+                    for (int i = 0; ok && i < cnt; ++i) {
+                        const int pg0 = __shfl_sync(0xffffffffu, page, 2 * i);
+                        const int pg1 = __shfl_sync(0xffffffffu, page, 2 * i + 1);
+                        load_tile(&kmap, g.h, pg0, pg1);
+                        if (ok && u + i == g.u_begin) {
+                            // the streams' Q behind the first keys, which need not wait for the last segment's end
+                            for (int st = 0; ok && st < 2; ++st) {
+                                const Stream s = stream_info(p, g, st);
+                                if (s.lo >= s.hi) continue;
+                                if (qn[st]) ok = mbar_wait(&q_empty[st], (qn[st] - 1) & 1, p.err, &abort_flag);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (!ok) break;
+                                if (lane == 0) {
+                                    const int tok = g.s.q0 + (g.x.row0 + st * (p.TM / 2)) / p.G;
+                                    mbar_expect_tx(&q_full[st], (p.TM / 2) * 128 * C::NH);
+#pragma unroll
+                                    for (int x = 0; x < C::NH; ++x)
+                                        tma_load_3d(Qs + st * C::TILE + x * C::BLOCK, &qmap, &q_full[st], x * 64, g.h * p.G,
+                                                    tok);
+                                }
+                                __syncwarp();
+                                ++qn[st];
+                            }
+                        }
+                        if (ok) load_tile(&vmap, g.h, pg0, pg1);
+                    }
+                }
+            }
+            // an abandoned run: copies in flight end before the block's shared memory does
+            if (!ok) {
+                for (uint32_t j = it > NST ? it - NST : 0; j < it; ++j)
+                    mbar_wait(&full[j % NST], (j / NST) & 1, p.err, nullptr);
+                for (int st = 0; st < 2; ++st)
+                    if (qn[st]) mbar_wait(&q_full[st], (qn[st] - 1) & 1, p.err, nullptr);
+            }
+        } else if (warp == MMA_WARP) {
+            // ---- matrix products: one lane issues; all lanes walk the units ----
+            constexpr uint32_t FMT = F16 ? 0 : 1;
+            constexpr uint32_t ID_S = idesc(FMT, FMT, 0, 0, UNIT, 128);
+            constexpr uint32_t ID_PV = idesc(FMT, FMT, 0, 1, D, 128);
+            const uint32_t qa = smem_u32(Qs), ra = smem_u32(ring);
+            uint32_t it = 0, qn[2] = {0, 0}, pn[2] = {0, 0};  // units; Q loads and P tiles waited for
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && mbar_wait(bar, parity, p.err, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            while (ok && next_segment<UNIT>(p, cur, g)) {
+                const Stream s0 = stream_info(p, g, 0), s1 = stream_info(p, g, 1);
+                for (int i = g.u_begin; ok && i <= g.u_end; ++i, ++it) {
+                    const bool has_s = i < g.u_end, has_pv = i > g.u_begin;
+                    const uint32_t ks = 2 * it, vs = 2 * it - 1;  // ring positions of K(i) and V(i-1)
+                    if (has_s && !wait(&full[ks % NST], (ks / NST) & 1)) break;
+                    const uint32_t ka = ra + (ks % NST) * C::TILE, va = ra + (vs % NST) * C::TILE;
+                    if (has_pv) {
+                        if (!wait(&full[vs % NST], (vs / NST) & 1)) break;
+                        // values at positions that no row of the tile sees may be anything: zeros instead
+                        const int key0 = (g.x.u0 + i - 1) * UNIT;
+                        if (key0 + UNIT > g.x.key_hi || key0 < g.x.key_lo) {
+                            uint8_t *v = ring + (vs % NST) * C::TILE;
+                            for (int c = lane; c < C::TILE / 16; c += 32) {
+                                const int key = key0 + ((c >> 3) & 127);
+                                if (key < g.x.key_lo || key >= g.x.key_hi)
+                                    *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        const Stream &s = st ? s1 : s0;
+                        if (has_pv && i - 1 >= s.lo && i - 1 < s.hi) {
+                            if (!wait(&p_full[st], pn[st] & 1)) break;
+                            ++pn[st];
+                            if (lane == 0) {
+#pragma unroll
+                                for (int k = 0; k < UNIT / 16; ++k)
+                                    mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128 + k * 8,
+                                           sdesc(va + 2048 * k, C::BLOCK, 1024, SWZ_128B), ID_PV, i - 1 > s.lo || k > 0);
+                                if (i == s.hi) mma_commit(&o_full[st]);
+                            }
+                            __syncwarp();
+                        }
+                        if (has_s && i >= s.lo && i < s.hi) {
+                            if (i == s.lo) {
+                                if (!wait(&q_full[st], qn[st] & 1)) break;
+                                ++qn[st];
+                            }
+                            if (lane == 0) {
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t o = (k >> 2) * C::BLOCK + (k & 3) * 32;
+                                    mma_bf16(tmem + st * 128, sdesc(qa + st * C::TILE + o, 16, 1024, SWZ_128B),
+                                             sdesc(ka + o, 16, 1024, SWZ_128B), ID_S, k > 0);
+                                }
+                                mma_commit(&s_full[st]);
+                                if (i + 1 == s.hi) mma_commit(&q_empty[st]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (ok && lane == 0) {
+                        if (has_pv) mma_commit(&empty[vs % NST]);
+                        if (has_s) mma_commit(&empty[ks % NST]);
+                    }
+                    __syncwarp();
+                }
+                --it;  // the last step had no keys of its own
+            }
+            // products in flight end before tensor and shared memory are given back
+            if (lane == 0) {
+                mma_commit(&drain);
+                mbar_wait(&drain, 0, p.err, nullptr);
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
+        // ---- softmax and output of stream st: thread r holds row r ----
+        const int st = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter: lane 32 x (warp % 4), bits 16 up
+        const uint32_t ts = tmem + lanes + st * 128, to = tmem + lanes + C::O_COL + st * 128;
+        const float c = p.scale_log2;
+        uint32_t sn = 0, on = 0;  // S tiles and outputs waited for
+        bool ok = true;
+        while (ok && next_segment<UNIT>(p, cur, g)) {
+            const Stream s = stream_info(p, g, st);
+            const bool have = r < s.rows;
+            const int tok = r / p.G, pos = have ? s.p_first + tok : -1;
+            float m = -INFINITY, l = 0.f;  // the reference that the weights refer to (raw scores), their sum
+            for (int i = s.lo; i < s.hi; ++i) {
+                ok = mbar_wait(&s_full[st], sn & 1, p.err, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++sn;
+                tc_fence_after();
+                uint32_t v[128];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, v + 32 * j);
+                tmem_wait_ld();
+                const int key0 = (g.x.u0 + i) * UNIT;
+                const bool edge = key0 + UNIT - 1 > s.p_first || (p.window && key0 <= s.p_last - p.window);
+                if (edge) {
+                    const int hi = pos - key0, lo = p.window ? hi - p.window : -1;  // key j is seen: lo < j <= hi
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j > hi || j <= lo) v[j] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[j + 2 * q])), __uint_as_float(v[j + 2 * q + 1]));
+                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                const bool grow = (top - m) * c > 8.f;  // (false where both are -inf)
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float nm = top, nu = nm == -INFINITY ? 0.f : nm;
+                    const float f = ex2_approx((m - nu) * c);
+                    m = nm;
+                    l *= f;
+                    if (i > s.lo) {
+                        // S(i) complete: so is the product before it, and O is still
+#pragma unroll
+                        for (int j = 0; j < D; j += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + j, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                            tmem_st32(to + j, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int j = 0; j < 128; j += 8) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint64_t x = fma2(pk(__uint_as_float(v[j + 2 * q]), __uint_as_float(v[j + 2 * q + 1])), c2, n2);
+                        float2 e;
+                        if (q == 3 && !edge) {
+                            e = ex2_poly(x);
+                        } else {
+                            e = upk(x);
+                            e.x = ex2_approx(e.x), e.y = ex2_approx(e.y);
+                        }
+                        sum[q & 1] = add2(sum[q & 1], pk(e.x, e.y));
+                        // weights rounded to the values' type; their sum is of the unrounded ones
+                        v[(j >> 1) + q] = paged_pack2<F16>(e.x, e.y);
+                    }
+                }
+                tmem_st32(ts, v);
+                tmem_st32(ts + 32, v + 32);
+                const float2 sa = upk(add2(sum[0], sum[1]));
+                l += sa.x + sa.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[st]);
+            }
+            if (!ok) break;
+            const bool some = s.lo < s.hi;
+            if (some) {
+                ok = mbar_wait(&o_full[st], on & 1, p.err, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++on;
+                tc_fence_after();
+            }
+            const bool whole = g.whole();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float ls = l > 0.f ? m * c + log2f(l) : -INFINITY;
+            const int64_t orow = (int64_t)(g.s.q0 + s.p_first - (g.s.L - g.s.n) + tok) * p.H + g.h * p.G + (r - tok * p.G);
+            const int64_t piece = ((int64_t)blockIdx.x * 2 + g.slot()) * p.TM + st * (p.TM / 2) + r;
+            if (have) {
+                if (!whole)
+                    p.part_l[piece] = ls;
+                else if (p.lse)
+                    p.lse[orow] = ls * 0.6931471805599453f;
+            }
+#pragma unroll
+            for (int j = 0; j < D; j += 32) {
+                uint32_t o[32];
+                if (some) {
+                    tmem_ld32(to + j, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int q = 0; q < 32; ++q) o[q] = l > 0.f ? __float_as_uint(__uint_as_float(o[q]) * inv) : 0u;
+                if (!have) continue;
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * D + j);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = paged_pack2<F16>(__uint_as_float(o[8 * q + 2 * e]), __uint_as_float(o[8 * q + 2 * e + 1]));
+                        dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + piece * D + j);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+            }
+            if (threadIdx.x == 0 && g.slot() == 1 && !whole)
+                p.rec[blockIdx.x] = PieceRec{1, g.b, g.h, g.t, cur.at - (g.u_end - g.u_begin) + g.x.nu, cur.total};
+            tc_fence_before();  // the reads of O before the next segment's first product, which waits for its weights
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool F16>
+dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    auto fn = paged_attn_tc_kernel<D, F16>;
+    // the roles' register shares draw on what the block was launched with
+    static const bool regs_ok = [fn] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, fn) == cudaSuccess && fa.numRegs == REG_LAUNCH;
+    }();
+    if (!regs_ok || !ensure_smem(reinterpret_cast<const void *>(fn), Cfg<D>::SMEM)) return DSA_ERR_CUDA;
+    CUtensorMap qm, km, vm;
+    if (!paged_kv_maps(*a.cache, a.pg.num_pages, &km, &vm)) return DSA_ERR_CUDA;
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.H, (uint64_t)p.T};
+    const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)(p.TM / 2 / p.G)};
+    const uint64_t hs = (uint64_t)(p.H > 1 ? p.q_head : D) * 2, ts = (uint64_t)(p.T > 1 ? p.q_token : D) * 2;
+    if (!make_tmap_3d(&qm, p.q, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, hs, ts, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+        return DSA_ERR_CUDA;
+    fn<<<nc, THREADS, Cfg<D>::SMEM, st>>>(qm, km, vm, p);
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+int paged_attn_tc_rows(int G) { return 2 * (128 / G) * G; }
+
+dsa_status launch_paged_attn_tc(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    const bool f16 = a.dtype == DSA_F16;
+    if (a.cache->Dk == 128) return f16 ? launch<128, true>(a, p, nc, st) : launch<128, false>(a, p, nc, st);
+    return f16 ? launch<64, true>(a, p, nc, st) : launch<64, false>(a, p, nc, st);
+}
+
+}  // namespace dsa
