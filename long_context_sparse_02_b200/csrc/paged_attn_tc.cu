@@ -56,6 +56,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// True in one thread of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Two fp32 values in one 64-bit register pair.
 __device__ __forceinline__ uint64_t pk(float a, float b) {
     uint64_t r;
@@ -118,6 +125,79 @@ __device__ __forceinline__ Stream stream_info(const PagedAttnParams &p, const Se
     return s;
 }
 
+// A softmax warp's place in the walk over the segments, and what it needs of the current one at its end.
+struct Walk {
+    Cursor cur;
+    int64_t end;
+    int b, h, t, whole, slot, row0;
+};
+
+// One row's scores of a unit (tensor memory, 128 columns at ts) to weights (over them, packed) under the
+// reference m, with their sum added to l.  EDGE: keys outside (lo, hi] of the unit are masked.
+template <int D, bool F16, bool EDGE>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int hi, int lo, bool first, float &m,
+                                             float &l) {
+    uint32_t v[128];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, v + 32 * j);
+    tmem_wait_ld();
+    if (EDGE) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+            if (j > hi || j <= lo) v[j] = 0xff800000u;
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < 128; j += 8)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[j + 2 * q])), __uint_as_float(v[j + 2 * q + 1]));
+    const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+    const bool grow = (top - m) * c > 8.f;  // (false where both are -inf)
+    if (__any_sync(0xffffffffu, grow)) {
+        const float f = ex2_approx((m - (top == -INFINITY ? 0.f : top)) * c);
+        m = top;
+        l *= f;
+        if (!first) {
+            // the scores are complete: so is the product before them, and O is still
+#pragma unroll
+            for (int j = 0; j < D; j += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + j, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                tmem_st16(to + j, o);
+            }
+        }
+    }
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 128; j += 8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint64_t x = fma2(pk(__uint_as_float(v[j + 2 * q]), __uint_as_float(v[j + 2 * q + 1])), c2, n2);
+            float2 e;
+            if (q == 3 && !EDGE) {
+                e = ex2_poly(x);
+            } else {
+                e = upk(x);
+                e.x = ex2_approx(e.x), e.y = ex2_approx(e.y);
+            }
+            sum[q & 1] = add2(sum[q & 1], pk(e.x, e.y));
+            // weights rounded to the values' type; their sum is of the unrounded ones
+            v[(j >> 1) + q] = paged_pack2<F16>(e.x, e.y);
+        }
+        if (j == 56) tmem_st32(ts, v);
+    }
+    tmem_st32(ts + 32, v + 32);
+    const float2 sa = upk(add2(sum[0], sum[1]));
+    l += sa.x + sa.y;
+    tmem_wait_st();
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -129,6 +209,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *ring = Qs + 2 * C::TILE;
     __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
     __shared__ uint32_t tmem_slot;
+    __shared__ Walk walk[8];
     __shared__ int abort_flag;
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
@@ -152,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     Segment g;
 
     if (warp >= 8) {
@@ -235,7 +316,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr uint32_t FMT = F16 ? 0 : 1;
             constexpr uint32_t ID_S = idesc(FMT, FMT, 0, 0, UNIT, 128);
             constexpr uint32_t ID_PV = idesc(FMT, FMT, 0, 1, D, 128);
-            const uint32_t qa = smem_u32(Qs), ra = smem_u32(ring);
+            // Descriptors differ in their start address alone (16-byte units in the low bits), and one elected
+            // thread issues: forming each from its address, in a branch on the lane, took 125 clocks a product
+            // instead of the 64 that it runs.
+            const uint64_t dq = sdesc(smem_u32(Qs), 16, 1024, SWZ_128B), dk = sdesc(smem_u32(ring), 16, 1024, SWZ_128B),
+                           dv = sdesc(smem_u32(ring), C::BLOCK, 1024, SWZ_128B);
             uint32_t it = 0, qn[2] = {0, 0}, pn[2] = {0, 0};  // units; Q loads and P tiles waited for
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -250,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const bool has_s = i < g.u_end, has_pv = i > g.u_begin;
                     const uint32_t ks = 2 * it, vs = 2 * it - 1;  // ring positions of K(i) and V(i-1)
                     if (has_s && !wait(&full[ks % NST], (ks / NST) & 1)) break;
-                    const uint32_t ka = ra + (ks % NST) * C::TILE, va = ra + (vs % NST) * C::TILE;
+                    const uint64_t kd = dk + (ks % NST) * (C::TILE >> 4), vd = dv + (vs % NST) * (C::TILE >> 4);
                     if (has_pv) {
                         if (!wait(&full[vs % NST], (vs / NST) & 1)) break;
                         // values at positions that no row of the tile sees may be anything: zeros instead
@@ -272,11 +357,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (has_pv && i - 1 >= s.lo && i - 1 < s.hi) {
                             if (!wait(&p_full[st], pn[st] & 1)) break;
                             ++pn[st];
-                            if (lane == 0) {
+                            if (elect_one()) {
+                                mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128, vd, ID_PV, i - 1 > s.lo);
 #pragma unroll
-                                for (int k = 0; k < UNIT / 16; ++k)
-                                    mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128 + k * 8,
-                                           sdesc(va + 2048 * k, C::BLOCK, 1024, SWZ_128B), ID_PV, i - 1 > s.lo || k > 0);
+                                for (int k = 1; k < UNIT / 16; ++k)
+                                    mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128 + k * 8, vd + (2048 >> 4) * k, ID_PV, 1);
                                 if (i == s.hi) mma_commit(&o_full[st]);
                             }
                             __syncwarp();
@@ -286,12 +371,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (!wait(&q_full[st], qn[st] & 1)) break;
                                 ++qn[st];
                             }
-                            if (lane == 0) {
+                            if (elect_one()) {
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k) {
                                     const uint32_t o = (k >> 2) * C::BLOCK + (k & 3) * 32;
-                                    mma_bf16(tmem + st * 128, sdesc(qa + st * C::TILE + o, 16, 1024, SWZ_128B),
-                                             sdesc(ka + o, 16, 1024, SWZ_128B), ID_S, k > 0);
+                                    mma_bf16(tmem + st * 128, dq + ((st * C::TILE + o) >> 4), kd + (o >> 4), ID_S, k > 0);
                                 }
                                 mma_commit(&s_full[st]);
                                 if (i + 1 == s.hi) mma_commit(&q_empty[st]);
@@ -299,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             __syncwarp();
                         }
                     }
-                    if (ok && lane == 0) {
+                    if (ok && elect_one()) {
                         if (has_pv) mma_commit(&empty[vs % NST]);
                         if (has_s) mma_commit(&empty[ks % NST]);
                     }
@@ -308,11 +392,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 --it;  // the last step had no keys of its own
             }
             // products in flight end before tensor and shared memory are given back
-            if (lane == 0) {
-                mma_commit(&drain);
-                mbar_wait(&drain, 0, p.err, nullptr);
-            }
+            if (elect_one()) mma_commit(&drain);
             __syncwarp();
+            mbar_wait(&drain, 0, p.err, nullptr);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
@@ -323,86 +405,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float c = p.scale_log2;
         uint32_t sn = 0, on = 0;  // S tiles and outputs waited for
         bool ok = true;
-        while (ok && next_segment<UNIT>(p, cur, g)) {
-            const Stream s = stream_info(p, g, st);
-            const bool have = r < s.rows;
-            const int tok = r / p.G, pos = have ? s.p_first + tok : -1;
+        // A row of scores needs 128 registers: the walk's state waits in shared memory meanwhile.
+        Walk &wk = walk[warp];
+        if (lane == 0) wk.cur = cur;
+        __syncwarp();
+        while (ok) {
+            int i, hi, key0, p_first, p_last, pos;
+            bool have;
+            {
+                Cursor cu = wk.cur;
+                const bool more = next_segment<UNIT>(p, cu, g);
+                __syncwarp();
+                if (!more) break;
+                const Stream s = stream_info(p, g, st);
+                have = r < s.rows;
+                const int tok = r / p.G;
+                pos = have ? s.p_first + tok : -1;
+                i = s.lo, hi = s.hi, key0 = (g.x.u0 + s.lo) * UNIT, p_first = s.p_first, p_last = s.p_last;
+                if (lane == 0) {
+                    wk.cur = cu;
+                    wk.end = cu.at - (g.u_end - g.u_begin) + g.x.nu;
+                    wk.b = g.b, wk.h = g.h, wk.t = g.t;
+                    wk.whole = g.whole(), wk.slot = g.slot();
+                    wk.row0 = g.s.q0 - (g.s.L - g.s.n);
+                }
+                __syncwarp();
+            }
+            const bool some = i < hi;
             float m = -INFINITY, l = 0.f;  // the reference that the weights refer to (raw scores), their sum
-            for (int i = s.lo; i < s.hi; ++i) {
+            for (bool first = true; i < hi; ++i, key0 += UNIT, first = false) {
                 ok = mbar_wait(&s_full[st], sn & 1, p.err, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++sn;
                 tc_fence_after();
-                uint32_t v[128];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, v + 32 * j);
-                tmem_wait_ld();
-                const int key0 = (g.x.u0 + i) * UNIT;
-                const bool edge = key0 + UNIT - 1 > s.p_first || (p.window && key0 <= s.p_last - p.window);
-                if (edge) {
-                    const int hi = pos - key0, lo = p.window ? hi - p.window : -1;  // key j is seen: lo < j <= hi
-#pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j > hi || j <= lo) v[j] = 0xff800000u;
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int j = 0; j < 128; j += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[j + 2 * q])), __uint_as_float(v[j + 2 * q + 1]));
-                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
-                const bool grow = (top - m) * c > 8.f;  // (false where both are -inf)
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float nm = top, nu = nm == -INFINITY ? 0.f : nm;
-                    const float f = ex2_approx((m - nu) * c);
-                    m = nm;
-                    l *= f;
-                    if (i > s.lo) {
-                        // S(i) complete: so is the product before it, and O is still
-#pragma unroll
-                        for (int j = 0; j < D; j += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + j, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-                            tmem_st32(to + j, o);
-                        }
-                    }
-                }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int j = 0; j < 128; j += 8) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint64_t x = fma2(pk(__uint_as_float(v[j + 2 * q]), __uint_as_float(v[j + 2 * q + 1])), c2, n2);
-                        float2 e;
-                        if (q == 3 && !edge) {
-                            e = ex2_poly(x);
-                        } else {
-                            e = upk(x);
-                            e.x = ex2_approx(e.x), e.y = ex2_approx(e.y);
-                        }
-                        sum[q & 1] = add2(sum[q & 1], pk(e.x, e.y));
-                        // weights rounded to the values' type; their sum is of the unrounded ones
-                        v[(j >> 1) + q] = paged_pack2<F16>(e.x, e.y);
-                    }
-                }
-                tmem_st32(ts, v);
-                tmem_st32(ts + 32, v + 32);
-                const float2 sa = upk(add2(sum[0], sum[1]));
-                l += sa.x + sa.y;
-                tmem_wait_st();
+                if (key0 + UNIT - 1 > p_first || (p.window && key0 <= p_last - p.window))
+                    softmax_tile<D, F16, true>(ts, to, c, pos - key0, p.window ? pos - key0 - p.window : -1, first, m, l);
+                else
+                    softmax_tile<D, F16, false>(ts, to, c, 0, 0, first, m, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[st]);
             }
             if (!ok) break;
-            const bool some = s.lo < s.hi;
             if (some) {
                 ok = mbar_wait(&o_full[st], on & 1, p.err, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -410,11 +455,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++on;
                 tc_fence_after();
             }
-            const bool whole = g.whole();
+            const bool whole = wk.whole;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const float ls = l > 0.f ? m * c + log2f(l) : -INFINITY;
-            const int64_t orow = (int64_t)(g.s.q0 + s.p_first - (g.s.L - g.s.n) + tok) * p.H + g.h * p.G + (r - tok * p.G);
-            const int64_t piece = ((int64_t)blockIdx.x * 2 + g.slot()) * p.TM + st * (p.TM / 2) + r;
+            const int tok = r / p.G;
+            const int64_t orow = (int64_t)(wk.row0 + p_first + tok) * p.H + wk.h * p.G + (r - tok * p.G);
+            const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + st * (p.TM / 2) + r;
             if (have) {
                 if (!whole)
                     p.part_l[piece] = ls;
@@ -447,8 +493,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
             }
-            if (threadIdx.x == 0 && g.slot() == 1 && !whole)
-                p.rec[blockIdx.x] = PieceRec{1, g.b, g.h, g.t, cur.at - (g.u_end - g.u_begin) + g.x.nu, cur.total};
+            if (threadIdx.x == 0 && wk.slot == 1 && !whole)
+                p.rec[blockIdx.x] = PieceRec{1, wk.b, wk.h, wk.t, wk.end, wk.cur.total};
+            __syncwarp();  // the walk's state is read before the next segment's is written
             tc_fence_before();  // the reads of O before the next segment's first product, which waits for its weights
         }
     }
