@@ -18,10 +18,7 @@
 // Tensor memory is full: S0 S1 O0 O1 at 128 columns each.  The running
 // maximum that the weights refer to is only moved when it has grown by more
 // than 2^8 (weights stay below 2^8, their sum is fp32, and the quotient does
-// not depend on the reference), so O is rarely rescaled.  The 16-per-clock
-// exponential unit would take as long as the two matrix products (2048 clocks
-// a unit at D = 128); a part of the exponentials goes to a degree-4 polynomial
-// on the FMA pipe instead.
+// not depend on the reference), so O is rarely rescaled.
 #include <cuda_fp16.h>
 
 #include "dsa_device.cuh"
@@ -33,7 +30,7 @@ namespace {
 
 constexpr int UNIT = 128;
 constexpr int THREADS = 384;  // two softmax warpgroups, one of single-warp roles
-constexpr int MMA_WARP = 8, LOAD_WARP = 9;
+constexpr int MMA_WARP = 8, LOAD_WARP = 9, CLEAR_WARP = 10;
 // registers: 384 x 168 at launch; the roles' shares add up to the same
 constexpr int REG_LAUNCH = 168, REG_SOFTMAX = 208, REG_REST = 88;
 static_assert(256 * REG_SOFTMAX + 128 * REG_REST == THREADS * REG_LAUNCH, "register shares");
@@ -85,25 +82,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// 2^x for two finite x <= 16: x = n + f with n the nearest integer (adding 1.5 x 2^23 leaves it in the
-// low bits), 2^f on [-1/2, 1/2] by the degree-4 polynomial of least relative error (2.7e-6 in fp32,
-// computed by exchange on that interval), n added to the exponent.  Below 2^-126: 2^-126.
-__device__ __forceinline__ float2 ex2_poly(uint64_t x2) {
-    float2 x = upk(x2);
-    x.x = fmaxf(x.x, -126.f), x.y = fmaxf(x.y, -126.f);
-    const uint64_t xc = pk(x.x, x.y);
-    const uint64_t t = add2(xc, pk(12582912.f, 12582912.f));
-    const uint64_t n = add2(t, pk(-12582912.f, -12582912.f));
-    const uint64_t f = fma2(n, pk(-1.f, -1.f), xc);
-    uint64_t p = fma2(pk(0.009570102207362652f, 0.009570102207362652f), f, pk(0.05591785907745361f, 0.05591785907745361f));
-    p = fma2(p, f, pk(0.240247443318367f, 0.240247443318367f));
-    p = fma2(p, f, pk(0.6931217908859253f, 0.6931217908859253f));
-    p = fma2(p, f, pk(0.9999992847442627f, 0.9999992847442627f));
-    const float2 pf = upk(p), tf = upk(t);
-    return make_float2(__uint_as_float(__float_as_uint(pf.x) + (__float_as_uint(tf.x) << 23)),
-                       __uint_as_float(__float_as_uint(pf.y) + (__float_as_uint(tf.y) << 23)));
-}
-
 // A stream's rows of a tile, and the segment's units that they see ([lo, hi), of the tile's units).
 struct Stream {
     int rows, lo, hi;
@@ -132,20 +110,38 @@ struct Walk {
     int b, h, t, whole, slot, row0;
 };
 
+// Half a row of scores (64 keys) to weights 2^(c s - mc), rounded to the values' type and packed into
+// out[0..31]; the sum of the unrounded ones.
+template <bool F16>
+__device__ __forceinline__ float weigh_half(const uint32_t *v, uint32_t *out, float c, float mc) {
+    const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float2 e = upk(fma2(pk(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, n2));
+        e.x = ex2_approx(e.x), e.y = ex2_approx(e.y);
+        sum[j & 1] = add2(sum[j & 1], pk(e.x, e.y));
+        out[j] = paged_pack2<F16>(e.x, e.y);
+    }
+    const float2 s = upk(add2(sum[0], sum[1]));
+    return s.x + s.y;
+}
+__device__ __forceinline__ void mask_half(uint32_t *v, int hi, int lo) {  // keys outside (lo, hi]
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+        if (j > hi || j <= lo) v[j] = 0xff800000u;
+}
+
 // One row's scores of a unit (tensor memory, 128 columns at ts) to weights (over them, packed) under the
-// reference m, with their sum added to l.  EDGE: keys outside (lo, hi] of the unit are masked.
+// reference m, with their sum added to l; `ready` is told.  EDGE: keys outside (lo, hi] of the unit are masked.
 template <int D, bool F16, bool EDGE>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int hi, int lo, bool first, float &m,
-                                             float &l) {
+                                             float &l, uint64_t *ready) {
     uint32_t v[128];
 #pragma unroll
     for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, v + 32 * j);
     tmem_wait_ld();
-    if (EDGE) {
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-            if (j > hi || j <= lo) v[j] = 0xff800000u;
-    }
+    if (EDGE) mask_half(v, hi, lo), mask_half(v + 64, hi - 64, lo - 64);
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int j = 0; j < 128; j += 8)
@@ -153,8 +149,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
         for (int q = 0; q < 4; ++q)
             mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[j + 2 * q])), __uint_as_float(v[j + 2 * q + 1]));
     const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
-    const bool grow = (top - m) * c > 8.f;  // (false where both are -inf)
-    if (__any_sync(0xffffffffu, grow)) {
+    if (__any_sync(0xffffffffu, (top - m) * c > 8.f)) {  // (false where both are -inf)
         const float f = ex2_approx((m - (top == -INFINITY ? 0.f : top)) * c);
         m = top;
         l *= f;
@@ -172,30 +167,19 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
         }
     }
     const float mc = m == -INFINITY ? 0.f : m * c;
-    const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
-    uint64_t sum[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 128; j += 8) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint64_t x = fma2(pk(__uint_as_float(v[j + 2 * q]), __uint_as_float(v[j + 2 * q + 1])), c2, n2);
-            float2 e;
-            if (q == 3 && !EDGE) {
-                e = ex2_poly(x);
-            } else {
-                e = upk(x);
-                e.x = ex2_approx(e.x), e.y = ex2_approx(e.y);
-            }
-            sum[q & 1] = add2(sum[q & 1], pk(e.x, e.y));
-            // weights rounded to the values' type; their sum is of the unrounded ones
-            v[(j >> 1) + q] = paged_pack2<F16>(e.x, e.y);
-        }
-        if (j == 56) tmem_st32(ts, v);
-    }
-    tmem_st32(ts + 32, v + 32);
-    const float2 sa = upk(add2(sum[0], sum[1]));
-    l += sa.x + sa.y;
+    l += weigh_half<F16>(v, v, c, mc);
+    tmem_st32(ts, v);
+    l += weigh_half<F16>(v + 64, v, c, mc);
+    tmem_st32(ts + 32, v);
     tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(ready);
+}
+
+// Whether a unit of the tile has positions that none of its rows sees.
+__device__ __forceinline__ bool needs_clear(const Segment &g, int key0) {
+    return key0 + UNIT > g.x.key_hi || key0 < g.x.key_lo;
 }
 
 template <int D, bool F16>
@@ -207,13 +191,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *Qs = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = Qs + 2 * C::TILE;
-    __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], v_clear[NST], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ Walk walk[8];
     __shared__ int abort_flag;
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int s = 0; s < NST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 2), mbar_init(&v_clear[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1), mbar_init(&p_full[s], 4), mbar_init(&o_full[s], 1);
@@ -312,89 +296,119 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (qn[st]) mbar_wait(&q_full[st], (qn[st] - 1) & 1, p.err, nullptr);
             }
         } else if (warp == MMA_WARP) {
-            // ---- matrix products: one lane issues; all lanes walk the units ----
-            constexpr uint32_t FMT = F16 ? 0 : 1;
-            constexpr uint32_t ID_S = idesc(FMT, FMT, 0, 0, UNIT, 128);
-            constexpr uint32_t ID_PV = idesc(FMT, FMT, 0, 1, D, 128);
-            // Descriptors differ in their start address alone (16-byte units in the low bits), and one elected
-            // thread issues: forming each from its address, in a branch on the lane, took 125 clocks a product
-            // instead of the 64 that it runs.
-            const uint64_t dq = sdesc(smem_u32(Qs), 16, 1024, SWZ_128B), dk = sdesc(smem_u32(ring), 16, 1024, SWZ_128B),
-                           dv = sdesc(smem_u32(ring), C::BLOCK, 1024, SWZ_128B);
-            uint32_t it = 0, qn[2] = {0, 0}, pn[2] = {0, 0};  // units; Q loads and P tiles waited for
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                ok = ok && mbar_wait(bar, parity, p.err, &abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok) tc_fence_after();
-                return ok;
-            };
-            while (ok && next_segment<UNIT>(p, cur, g)) {
-                const Stream s0 = stream_info(p, g, 0), s1 = stream_info(p, g, 1);
-                for (int i = g.u_begin; ok && i <= g.u_end; ++i, ++it) {
-                    const bool has_s = i < g.u_end, has_pv = i > g.u_begin;
-                    const uint32_t ks = 2 * it, vs = 2 * it - 1;  // ring positions of K(i) and V(i-1)
-                    if (has_s && !wait(&full[ks % NST], (ks / NST) & 1)) break;
-                    const uint64_t kd = dk + (ks % NST) * (C::TILE >> 4), vd = dv + (vs % NST) * (C::TILE >> 4);
-                    if (has_pv) {
-                        if (!wait(&full[vs % NST], (vs / NST) & 1)) break;
-                        // values at positions that no row of the tile sees may be anything: zeros instead
-                        const int key0 = (g.x.u0 + i - 1) * UNIT;
-                        if (key0 + UNIT > g.x.key_hi || key0 < g.x.key_lo) {
-                            uint8_t *v = ring + (vs % NST) * C::TILE;
-                            for (int c = lane; c < C::TILE / 16; c += 32) {
-                                const int key = key0 + ((c >> 3) & 127);
-                                if (key < g.x.key_lo || key >= g.x.key_hi)
-                                    *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
+            // ---- matrix products: one thread.  What it does between two products is seen by the tensor pipe (its
+            // queue is short), so it does little: descriptors differ in their start address alone (16-byte units
+            // in the low bits), ring positions are counted along, and values are cleared by another warp. ----
+            if (elect_one()) {
+                constexpr uint32_t FMT = F16 ? 0 : 1;
+                constexpr uint32_t ID_S = idesc(FMT, FMT, 0, 0, UNIT, 128);
+                constexpr uint32_t ID_PV = idesc(FMT, FMT, 0, 1, D, 128);
+                const uint64_t dq = sdesc(smem_u32(Qs), 16, 1024, SWZ_128B), dk = sdesc(smem_u32(ring), 16, 1024, SWZ_128B),
+                               dv = sdesc(smem_u32(ring), C::BLOCK, 1024, SWZ_128B);
+                int slot = 0, vslot = 0;  // ring positions of K(i) and V(i-1), and the parity of their use
+                uint32_t par = 0, vpar = 0, qpar[2] = {0, 0}, ppar[2] = {0, 0}, cpar = 0;
+                bool ok = true;
+                auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = mbar_wait(bar, parity, p.err, &abort_flag); };
+                auto advance = [&] {
+                    if (++slot == NST) slot = 0, par ^= 1;
+                };
+                while (ok && next_segment<UNIT>(p, cur, g)) {
+                    const Stream s0 = stream_info(p, g, 0), s1 = stream_info(p, g, 1);
+                    const int key_u0 = g.x.u0 * UNIT;
+                    for (int i = g.u_begin; i <= g.u_end; ++i) {
+                        const bool has_s = i < g.u_end, has_pv = i > g.u_begin;
+                        const int kslot = slot;
+                        if (has_s) {
+                            if (!wait(&full[kslot], par)) break;
+                            advance();
                         }
-                    }
+                        if (has_pv) {
+                            if (!wait(&full[vslot], vpar)) break;
+                            const int key0 = key_u0 + (i - 1) * UNIT;
+                            if (needs_clear(g, key0)) {
+                                // (a barrier a slot: the clearing warp may be two cleared units ahead)
+                                if (!wait(&v_clear[vslot], (cpar >> vslot) & 1)) break;
+                                cpar ^= 1u << vslot;
+                            }
+                        }
+                        const uint64_t kd = dk + kslot * (C::TILE >> 4), vd = dv + vslot * (C::TILE >> 4);
 #pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        const Stream &s = st ? s1 : s0;
-                        if (has_pv && i - 1 >= s.lo && i - 1 < s.hi) {
-                            if (!wait(&p_full[st], pn[st] & 1)) break;
-                            ++pn[st];
-                            if (elect_one()) {
-                                mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128, vd, ID_PV, i - 1 > s.lo);
+                        for (int st = 0; st < 2; ++st) {
+                            const int lo = st ? s1.lo : s0.lo, hi = st ? s1.hi : s0.hi;
+                            if (has_pv && i - 1 >= lo && i - 1 < hi) {
+                                if (!wait(&p_full[st], ppar[st])) break;
+                                ppar[st] ^= 1;
+                                tc_fence_after();
+                                mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128, vd, ID_PV, i - 1 > lo);
 #pragma unroll
                                 for (int k = 1; k < UNIT / 16; ++k)
                                     mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128 + k * 8, vd + (2048 >> 4) * k, ID_PV, 1);
-                                if (i == s.hi) mma_commit(&o_full[st]);
+                                if (i == hi) mma_commit(&o_full[st]);
                             }
-                            __syncwarp();
-                        }
-                        if (has_s && i >= s.lo && i < s.hi) {
-                            if (i == s.lo) {
-                                if (!wait(&q_full[st], qn[st] & 1)) break;
-                                ++qn[st];
-                            }
-                            if (elect_one()) {
+                            if (has_s && i >= lo && i < hi) {
+                                if (i == lo) {
+                                    if (!wait(&q_full[st], qpar[st])) break;
+                                    qpar[st] ^= 1;
+                                }
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k) {
                                     const uint32_t o = (k >> 2) * C::BLOCK + (k & 3) * 32;
                                     mma_bf16(tmem + st * 128, dq + ((st * C::TILE + o) >> 4), kd + (o >> 4), ID_S, k > 0);
                                 }
                                 mma_commit(&s_full[st]);
-                                if (i + 1 == s.hi) mma_commit(&q_empty[st]);
+                                if (i + 1 == hi) mma_commit(&q_empty[st]);
                             }
-                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        if (has_pv) mma_commit(&empty[vslot]);
+                        if (has_s) {
+                            mma_commit(&empty[kslot]);
+                            vslot = slot, vpar = par;  // V(i) follows K(i)
+                            advance();
                         }
                     }
-                    if (ok && elect_one()) {
-                        if (has_pv) mma_commit(&empty[vs % NST]);
-                        if (has_s) mma_commit(&empty[ks % NST]);
-                    }
-                    __syncwarp();
                 }
-                --it;  // the last step had no keys of its own
+                // products in flight end before tensor and shared memory are given back
+                mma_commit(&drain);
+                mbar_wait(&drain, 0, p.err, nullptr);
             }
-            // products in flight end before tensor and shared memory are given back
-            if (elect_one()) mma_commit(&drain);
             __syncwarp();
-            mbar_wait(&drain, 0, p.err, nullptr);
+        } else if (warp == CLEAR_WARP) {
+            // ---- values at positions that no row of the tile sees may be anything (unwritten rows, other
+            // sequences'): weights of 0 do not silence a NaN, so they are set to zero before their product ----
+            int slot = 0;
+            uint32_t par = 0;
+            bool ok = true;
+            auto next = [&] {  // every position is waited for and released: its parity tells one use from the next
+                ok = ok && mbar_wait(&full[slot], par, p.err, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                return ok;
+            };
+            auto release = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
+                if (++slot == NST) slot = 0, par ^= 1;
+            };
+            while (ok && next_segment<UNIT>(p, cur, g)) {
+                for (int i = g.u_begin; i < g.u_end; ++i) {
+                    if (!next()) break;
+                    release();  // keys
+                    if (!next()) break;
+                    const int key0 = (g.x.u0 + i) * UNIT;
+                    if (needs_clear(g, key0)) {
+                        uint8_t *v = ring + slot * C::TILE;
+                        for (int x = lane; x < C::TILE / 16; x += 32) {
+                            const int key = key0 + ((x >> 3) & 127);
+                            if (key < g.x.key_lo || key >= g.x.key_hi)
+                                *reinterpret_cast<uint4 *>(v + x * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&v_clear[slot]);
+                    }
+                    release();
+                }
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
@@ -440,12 +454,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++sn;
                 tc_fence_after();
                 if (key0 + UNIT - 1 > p_first || (p.window && key0 <= p_last - p.window))
-                    softmax_tile<D, F16, true>(ts, to, c, pos - key0, p.window ? pos - key0 - p.window : -1, first, m, l);
+                    softmax_tile<D, F16, true>(ts, to, c, pos - key0, p.window ? pos - key0 - p.window : -1, first, m, l,
+                                                 &p_full[st]);
                 else
-                    softmax_tile<D, F16, false>(ts, to, c, 0, 0, first, m, l);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[st]);
+                    softmax_tile<D, F16, false>(ts, to, c, 0, 0, first, m, l,
+                                                 &p_full[st]);
             }
             if (!ok) break;
             if (some) {
