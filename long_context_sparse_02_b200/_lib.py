@@ -115,16 +115,14 @@ lib.dsa_rope_frequencies.restype = ctypes.c_int
 lib.dsa_rope_frequencies.argtypes = [I32, ctypes.c_double, I32, ctypes.c_double, I32, ctypes.POINTER(ctypes.c_double),
                                      ctypes.POINTER(F32)]
 lib.dsa_rope.restype = ctypes.c_int
-lib.dsa_rope.argtypes = [P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I32, I32, I32,
-                         ctypes.POINTER(RopeSpec), P]
+# (structs of the calls below by address: see _addr)
+lib.dsa_rope.argtypes = [P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I32, I32, I32, P, P]
 lib.dsa_append_rope.restype = ctypes.c_int
-lib.dsa_append_rope.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, P, ctypes.POINTER(Paged), I32,
-                                I32, ctypes.POINTER(RopeSpec), ctypes.POINTER(KvCache), P]
+lib.dsa_append_rope.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, P, P, I32, I32, P, P, P]
 lib.dsa_paged_attn_workspace_bytes.restype = SZ
 lib.dsa_paged_attn_workspace_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(KvCache), I32, I32, I32]
 lib.dsa_paged_attn.restype = ctypes.c_int
-lib.dsa_paged_attn.argtypes = [P, I64, I64, I32, ctypes.POINTER(KvCache), ctypes.POINTER(Paged), P, I32, I32, I32, I32,
-                               F32, I32, P, P, P, SZ, P]
+lib.dsa_paged_attn.argtypes = [P, I64, I64, I32, P, P, P, I32, I32, I32, I32, F32, I32, P, P, P, SZ, P]
 
 EXPORTS = ["dsa_abi_version", "dsa_status_string", "dsa_device_error", "dsa_indexer_scores", "dsa_indexer_scores_mx",
            "dsa_append_kv_mx",
@@ -376,34 +374,62 @@ _IO = {torch.bfloat16: BF16, torch.float16: F16}
 _CACHE = {torch.bfloat16: BF16, torch.float16: F16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}
 
 
-def _on(device: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+# These calls are made once a layer and step: the checks read each tensor's facts once and the arguments go over as
+# plain integers (a decode step's rotation took 17 us of host time otherwise, most of it spent on wrappers).
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without the Stream object
 
 
-def _call(fn: str, device: torch.device, *args):
-    """The library call on `device`'s current stream, with that device current."""
-    f = getattr(lib, fn)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
-    return _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
-
-
-def _heads(t, name: str, dtype=None, heads=None, width=None):
-    """[T, heads, D] with a contiguous last dimension: (pointer, token stride, head stride)."""
-    if not t.is_cuda:
+def _device(t, name: str) -> int:
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (t.dtype not in _IO if dtype is None else t.dtype != dtype):
-        raise ValueError(f"{name} must be a {dtype or 'bf16 or fp16'} tensor [tokens, heads, width], got "
-                         f"{t.dtype} {tuple(t.shape)}")
-    if (heads is not None and t.shape[1] != heads) or (width is not None and t.shape[2] != width):
-        raise ValueError(f"{name} must have {heads} heads of {width}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1 and t.shape[2] > 1:
+    return d
+
+
+def _on(dev: int, name: str, t):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _call(fn: str, f, dev: int, *args):
+    """The library call on device dev's current stream, with that device current."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        status = f(*args, _raw_stream(dev))
+        if status:
+            raise DsaError(fn, status)
+
+
+def _addr(struct) -> int:
+    return ctypes.addressof(struct)
+
+
+def _heads(t, name: str, dev: int, dtype, shape):
+    """[tokens, heads, width] with a contiguous last dimension: (pointer, token stride, head stride)."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and shape[2] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr(), st[0], st[1]
+    return t.data_ptr(), ts, hs
+
+
+def _first(t, name: str):
+    """(device, dtype, tokens, heads, width) of the tensor that the others of a call go by."""
+    dev = _device(t, name)
+    if t.dim() != 3 or t.dtype not in _IO:
+        raise ValueError(f"{name} must be a bf16 or fp16 tensor [tokens, heads, width], got {t.dtype} {tuple(t.shape)}")
+    return (dev, t.dtype, *t.shape)
+
+
+def _tokens(t, name: str, dev: int, n: int) -> int:
+    if t.get_device() != dev or t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def rope_frequencies(dim: int, base: float = 10000.0, scheme: str = "plain", scale: float = 1.0, orig_len: int = 0):
@@ -425,6 +451,7 @@ def rope_spec(inv_freq: torch.Tensor, offset: int = 0, interleaved: bool = False
     spec = RopeSpec(_ptr(inv_freq, torch.float64, "inv_freq"), 2 * int(inv_freq.numel()), int(offset),
                     ROPE_INTERLEAVED if interleaved else ROPE_HALF, int(bool(inverse)), float(factor))
     spec._tensors = (inv_freq,)
+    spec._device = inv_freq.get_device()
     return spec
 
 
@@ -443,75 +470,64 @@ def kv_cache(k: torch.Tensor, v: torch.Tensor = None, k_scale: float = 1.0, v_sc
     c = KvCache(k.data_ptr(), v.data_ptr() if v is not None else None, *k.stride()[:3], *sv[:3], int(k.shape[2]),
                 int(k.shape[3]), int(v.shape[3]) if v is not None else 0, _CACHE[k.dtype], float(k_scale), float(v_scale))
     c._tensors = (k, v)
+    c._device, c._pages = k.get_device(), int(k.shape[0])
     return c
 
 
-def _cache_fits(cache: KvCache, pg: Paged, device):
-    k = cache._tensors[0]
-    if k.shape[0] < pg.num_pages:
-        raise ValueError(f"the cache has {k.shape[0]} pages, the page table {pg.num_pages}")
-    _on(device, cache=k, seq_lens=pg._tensors[0], block_table=pg._tensors[1])
+def _cache_fits(cache: KvCache, pg: Paged, dev: int):
+    if cache._pages < pg.num_pages:
+        raise ValueError(f"the cache has {cache._pages} pages, the page table {pg.num_pages}")
+    if cache._device != dev:
+        raise ValueError(f"the cache must be on cuda:{dev}")
+    _on(dev, "seq_lens", pg._tensors[0])
+    _on(dev, "block_table", pg._tensors[1])
 
 
-def _tokens(t, name: str, n: int):
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    return _ptr(t, torch.int32, name)
+def _spec_fits(spec: RopeSpec, dev: int) -> int:
+    if spec._device != dev:
+        raise ValueError(f"inv_freq must be on cuda:{dev}")
+    return ctypes.addressof(spec)
 
 
 def rope(q, pos, spec: RopeSpec, k=None, q_out=None, k_out=None):
     """Rotary positions on q [T, H, D] and (optionally, in the same launch) k [T, Hk, D], bf16 or fp16, at pos int32 [T].
     q_out / k_out default to new dense tensors; pass q / k themselves to rotate in place.  Returns (q_out, k_out)."""
-    T, H, D = q.shape
-    qa = _heads(q, "q")
-    _on(q.device, pos=pos, k=k, q_out=q_out, k_out=k_out, inv_freq=spec._tensors[0])
+    dev, dtype, T, H, D = _first(q, "q")
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
+        q_out = q.new_empty((T, H, D))
     ka, ko, Hk = (None, 0, 0), (None, 0, 0), 0
     if k is not None:
-        ka, Hk = _heads(k, "k", q.dtype, width=D, heads=k.shape[1]), int(k.shape[1])
-        if k.shape[0] != T:
-            raise ValueError("k must have q's tokens")
+        if k.dim() != 3:
+            raise ValueError("k must be [tokens, heads, width]")
+        Hk = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        ko = _heads(k_out, "k_out", q.dtype)
-    _call("dsa_rope", q.device, *qa, H, *_heads(q_out, "q_out", q.dtype), *ka, Hk, *ko, _tokens(pos, "pos", T), T, D,
-          _IO[q.dtype], ctypes.byref(spec))
+            k_out = k.new_empty((T, Hk, D))
+        ka, ko = _heads(k, "k", dev, dtype, (T, Hk, D)), _heads(k_out, "k_out", dev, dtype, (T, Hk, D))
+    _call("dsa_rope", lib.dsa_rope, dev, *_heads(q, "q", dev, dtype, (T, H, D)), H,
+          *_heads(q_out, "q_out", dev, dtype, (T, H, D)), *ka, Hk, *ko, _tokens(pos, "pos", dev, T), T, D, _IO[dtype],
+          _spec_fits(spec, dev))
     return q_out, k_out
 
 
 def append_rope(k_new, v_new, tok_seq, tok_pos, pg: Paged, cache: KvCache, spec: RopeSpec = None, q=None, q_out=None):
     """k_new [n, heads, Dk] (rotated to tok_pos) and v_new [n, heads, Dv] or None into the cache; q [n, H, Dk], where given,
     rotated in the same launch into q_out (default: a new dense tensor; q itself for in place), which is returned."""
-    n = k_new.shape[0]
-    ka = _heads(k_new, "k_new", None, cache.heads, cache.Dk)
-    dtype, dev = k_new.dtype, k_new.device
-    _on(dev, v_new=v_new, tok_seq=tok_seq, tok_pos=tok_pos, q=q, q_out=q_out)
+    dev, dtype, n, _, _ = _first(k_new, "k_new")
     _cache_fits(cache, pg, dev)
-    va = (None, 0, 0)
-    if v_new is not None:
-        if v_new.shape[0] != n:
-            raise ValueError("v_new must have k_new's tokens")
-        va = _heads(v_new, "v_new", dtype, cache.heads, cache.Dv)
+    heads, Dk = cache.heads, cache.Dk
+    ka = _heads(k_new, "k_new", dev, dtype, (n, heads, Dk))
+    va = (None, 0, 0) if v_new is None else _heads(v_new, "v_new", dev, dtype, (n, heads, cache.Dv))
     qa, qo, H = (None, 0, 0), (None, 0, 0), 0
     if q is not None:
-        if q.shape[0] != n:
-            raise ValueError("q must have k_new's tokens")
-        H = int(q.shape[1])
-        qa = _heads(q, "q", dtype, H, cache.Dk)
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads, width]")
+        H = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n, H, cache.Dk), dtype=dtype, device=dev)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        qo = _heads(q_out, "q_out", dtype)
-    if spec is not None:
-        _on(dev, inv_freq=spec._tensors[0])
-    _call("dsa_append_rope", dev, *ka, *va, *qa, H, *qo, _tokens(tok_seq, "tok_seq", n), _tokens(tok_pos, "tok_pos", n),
-          ctypes.byref(pg), n, _IO[dtype], ctypes.byref(spec) if spec is not None else None, ctypes.byref(cache))
+            q_out = q.new_empty((n, H, Dk))
+        qa, qo = _heads(q, "q", dev, dtype, (n, H, Dk)), _heads(q_out, "q_out", dev, dtype, (n, H, Dk))
+    _call("dsa_append_rope", lib.dsa_append_rope, dev, *ka, *va, *qa, H, *qo, _tokens(tok_seq, "tok_seq", dev, n),
+          _tokens(tok_pos, "tok_pos", dev, n), _addr(pg), n, _IO[dtype], None if spec is None else _spec_fits(spec, dev),
+          _addr(cache))
     return q_out if q is not None else None
 
 
@@ -528,23 +544,25 @@ def paged_attn(q, cache: KvCache, pg: Paged, q_start, max_q: int, max_len: int, 
                want_lse: bool = False, out=None, lse=None, ws=None):
     """Attention of q [T, H, D], each sequence's newest tokens (rows q_start[b] .. q_start[b+1], int32 [num_seqs + 1]; None:
     one each), over the paged cache, causal, optionally within a window.  Returns out, or (out, lse) with want_lse."""
-    T, H, D = q.shape
-    qa = _heads(q, "q", None, H, cache.Dk)
-    dev = q.device
-    _on(dev, q_start=q_start, out=out, lse=lse, ws=ws)
+    dev, dtype, T, H, D = _first(q, "q")
     _cache_fits(cache, pg, dev)
+    if D != cache.Dk:
+        raise ValueError(f"q must have heads of {cache.Dk}, got {D}")
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out must be dense, with q's shape and dtype")
-    if lse is None and want_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    elif lse is not None and tuple(lse.shape) != (T, H):
-        raise ValueError(f"lse must be [{T}, {H}]")
+        out = q.new_empty((T, H, D))
+    elif out.get_device() != dev or out.dtype != dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be dense, with q's shape, dtype and device")
+    if lse is None:
+        if want_lse:
+            lse = q.new_empty((T, H), dtype=torch.float32)
+    elif lse.get_device() != dev or lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a dense fp32 tensor [{T}, {H}] on cuda:{dev}")
     if ws is None:
         ws = paged_attn_workspace(T, H, cache, pg, max_q, max_len, window)
-    _call("dsa_paged_attn", dev, *qa, H, ctypes.byref(cache), ctypes.byref(pg),
-          None if q_start is None else _tokens(q_start, "q_start", pg.num_seqs + 1), T, max_q, max_len, window,
-          D ** -0.5 if sm_scale is None else sm_scale, _IO[q.dtype], out.data_ptr(),
-          _ptr(lse, torch.float32, "lse", True), ws.data_ptr(), ws.numel())
-    return (out, lse) if lse is not None else out
+    elif ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a dense uint8 tensor on cuda:{dev}")
+    _call("dsa_paged_attn", lib.dsa_paged_attn, dev, *_heads(q, "q", dev, dtype, (T, H, D)), H, _addr(cache), _addr(pg),
+          None if q_start is None else _tokens(q_start, "q_start", dev, pg.num_seqs + 1), T, max_q, max_len, window,
+          D ** -0.5 if sm_scale is None else sm_scale, _IO[dtype], out.data_ptr(), None if lse is None else lse.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return out if lse is None else (out, lse)

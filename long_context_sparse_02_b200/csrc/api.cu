@@ -612,6 +612,7 @@ dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_
     if (!cache->v || cache->Dk != cache->Dv || (cache->Dk != 64 && cache->Dk != 128) || H % cache->heads)
         return DSA_ERR_UNSUPPORTED;
     if (T == 0) return DSA_OK;
+    if ((int64_t)T * H >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     if ((T > 1 && (q_token_stride & 7)) || (H > 1 && (q_head_stride & 7))) return DSA_ERR_INVALID_ARG;
     PagedAttnArgs a{{q, q_token_stride, H > 1 ? q_head_stride : 0, H}, cache, paged_dev(pg), q_start, T, max_q,

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int r = 0; r < 2; ++r) {
             const int row = rbase + gid + 8 * r;
             have[r] = row < last_row;
-            const int tok = row / p.G, hg = row - tok * p.G;
+            const int tok = p.by_G.div(row), hg = row - tok * p.G;
             pos[r] = have[r] ? g.s.L - g.s.n + tok : -1;
             const uint16_t *src = static_cast<const uint16_t *>(p.q) + (int64_t)(g.s.q0 + tok) * p.q_token +
                                   (int64_t)(g.h * p.G + hg) * p.q_head;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 if (!have[r]) continue;
-                const int row = rbase + gid + 8 * r, tok = row / p.G, hg = row - tok * p.G;
+                const int row = rbase + gid + 8 * r, tok = p.by_G.div(row), hg = row - tok * p.G;
                 const float inv = l[r] > 0.f ? p.v_inv / l[r] : 0.f;
                 const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) : -INFINITY;
                 const int64_t orow = (int64_t)(g.s.q0 + tok) * p.H + g.h * p.G + hg;
@@ -459,28 +459,53 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
     const int row0 = rec.t * p.TM, rows = min(p.TM, s.n * p.G - row0);
     const int r = blockIdx.y * JOIN_WARPS + warp_id();
     if (r >= rows) return;
-    int last = c + 1;  // pieces: slot 1 of c, slot 0 of c + 1 .. last - 1
-    while (last < nc && line_start(rec.total, last, nc) < rec.end) ++last;
+    const Line line(rec.total, nc);
+    const int last = min(line.next(rec.end), nc);  // pieces: slot 1 of c, slot 0 of c + 1 .. last - 1
     auto at = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.TM + r; };
-    float mx = -INFINITY;
-    for (int i = c; i < last; ++i)
-        if (i == c || line_start(rec.total, i, nc) < line_start(rec.total, i + 1, nc)) mx = fmaxf(mx, p.part_l[at(i)]);
     constexpr int V = D / 32;
-    float acc[V], sum = 0.f;
+    float acc[V], sum = 0.f, mx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    if (mx != -INFINITY) {
-        for (int i = c; i < last; ++i) {
-            if (i != c && line_start(rec.total, i, nc) >= line_start(rec.total, i + 1, nc)) continue;
-            const float w = ex2_approx(p.part_l[at(i)] - mx);
-            const float *o = p.part_o + at(i) * D + lane * V;
-            sum += w;
+    for (int base = c; base < last; base += 32) {  // 32 pieces at a time, a lane each for their weights
+        const int mine = base + lane;
+        const float ls = mine < last && (mine == c || line.start(mine) < line.start(mine + 1)) ? p.part_l[at(mine)] : -INFINITY;
+        float top = ls;
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] = fmaf(w, o[j], acc[j]);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, mx);
+        if (top == -INFINITY) continue;
+        const float f = ex2_approx(mx - top), w = ex2_approx(ls - top);
+        mx = top;
+        sum *= f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] *= f;
+        const int cnt = min(32, last - base);
+        for (int i0 = 0; i0 < cnt; i0 += 8) {  // eight rows in flight
+            float o[8][V];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+                const bool some = i0 + i < cnt && wi > 0.f;  // (a piece without weight may be unwritten)
+                const float *src = p.part_o + at(base + i0 + i) * D + lane * V;
+                if (V == 4) {
+                    const float4 t = some ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    o[i][0] = t.x, o[i][1] = t.y, o[i][V - 2] = t.z, o[i][V - 1] = t.w;
+                } else {
+                    const float2 t = some ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
+                    o[i][0] = t.x, o[i][1] = t.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float wi = i0 + i < cnt ? __shfl_sync(0xffffffffu, w, (i0 + i) & 31) : 0.f;
+                sum += wi;
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] = fmaf(wi, o[i][j], acc[j]);
+            }
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int row = row0 + r, tok = row / p.G;
+    const int row = row0 + r, tok = p.by_G.div(row);
     const int64_t orow = (int64_t)(s.q0 + tok) * p.H + rec.h * p.G + (row - tok * p.G);
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow * D + lane * V);
 #pragma unroll
@@ -609,6 +634,7 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     p.q = a.q.data, p.q_token = a.q.token_stride, p.q_head = a.q.head_stride;
     p.q_start = a.q_start, p.pg = a.pg;
     p.T = a.T, p.H = H, p.Hkv = c.heads, p.G = G, p.TM = pl.TM;
+    p.by_G = FastDiv::of(G), p.by_TM = FastDiv::of(pl.TM);
     p.max_q = a.max_q, p.max_len = a.max_len, p.window = a.window;
     p.scale_log2 = (float)(a.sm_scale * 1.4426950408889634 / (e4m3 ? c.k_scale : 1.f));
     p.v_inv = e4m3 ? 1.f / c.v_scale : 1.f;

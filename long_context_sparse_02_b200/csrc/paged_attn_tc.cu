@@ -30,7 +30,7 @@ namespace {
 
 constexpr int UNIT = 128;
 constexpr int THREADS = 384;  // two softmax warpgroups, one of single-warp roles
-constexpr int MMA_WARP = 8, LOAD_WARP = 9, CLEAR_WARP = 10;
+constexpr int MMA_WARP = 8, LOAD_WARP = 10, CLEAR_WARP = 11;  // MMA_WARP + stream
 // registers: 384 x 168 at launch; the roles' shares add up to the same
 constexpr int REG_LAUNCH = 168, REG_SOFTMAX = 208, REG_REST = 88;
 static_assert(256 * REG_SOFTMAX + 128 * REG_REST == THREADS * REG_LAUNCH, "register shares");
@@ -92,8 +92,8 @@ __device__ __forceinline__ Stream stream_info(const PagedAttnParams &p, const Se
     const int rs = p.TM / 2, r0 = g.x.row0 + st * rs;
     s.rows = min(max(g.x.rows - st * rs, 0), rs);
     s.lo = s.hi = g.u_begin;
-    s.p_first = g.s.L - g.s.n + r0 / p.G;
-    s.p_last = s.p_first + s.rows / p.G - 1;  // rows are whole tokens
+    s.p_first = g.s.L - g.s.n + p.by_G.div(r0);
+    s.p_last = s.p_first + p.by_G.div(s.rows) - 1;  // rows are whole tokens
     s.key_hi = max(s.p_last + 1, 0);
     s.key_lo = p.window ? max(s.p_first - p.window + 1, 0) : 0;
     if (s.rows > 0 && s.key_hi > s.key_lo) {
@@ -110,14 +110,14 @@ struct Walk {
     int b, h, t, whole, slot, row0;
 };
 
-// Half a row of scores (64 keys) to weights 2^(c s - mc), rounded to the values' type and packed into
-// out[0..31]; the sum of the unrounded ones.
+// 32 scores to weights 2^(c s - mc), rounded to the values' type and packed into out[0..15]; the sum of the
+// unrounded ones.
 template <bool F16>
-__device__ __forceinline__ float weigh_half(const uint32_t *v, uint32_t *out, float c, float mc) {
+__device__ __forceinline__ float weigh(const uint32_t *v, uint32_t *out, float c, float mc) {
     const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 16; ++j) {
         float2 e = upk(fma2(pk(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, n2));
         e.x = ex2_approx(e.x), e.y = ex2_approx(e.y);
         sum[j & 1] = add2(sum[j & 1], pk(e.x, e.y));
@@ -126,36 +126,62 @@ __device__ __forceinline__ float weigh_half(const uint32_t *v, uint32_t *out, fl
     const float2 s = upk(add2(sum[0], sum[1]));
     return s.x + s.y;
 }
-__device__ __forceinline__ void mask_half(uint32_t *v, int hi, int lo) {  // keys outside (lo, hi]
+__device__ __forceinline__ float max32(const uint32_t *v) {
+    float mx[4];
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-        if (j > hi || j <= lo) v[j] = 0xff800000u;
+    for (int q = 0; q < 4; ++q) {
+        mx[q] = fmaxf(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+#pragma unroll
+        for (int j = 8; j < 32; j += 8)
+            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[j + 2 * q])), __uint_as_float(v[j + 2 * q + 1]));
+    }
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
-// One row's scores of a unit (tensor memory, 128 columns at ts) to weights (over them, packed) under the
-// reference m, with their sum added to l; `ready` is told.  EDGE: keys outside (lo, hi] of the unit are masked.
-template <int D, bool F16, bool EDGE>
-__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int hi, int lo, bool first, float &m,
-                                             float &l, uint64_t *ready) {
-    uint32_t v[128];
+// 32 bytes to global memory: one store, so that no sector is written in two halves, where the address allows.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// What a warp's rows see of a unit: nothing of the chunks of 32 keys in `none`, all of those in neither mask,
+// and of the others each row the keys in (lo, hi] of the unit.
+struct Sight {
+    uint32_t none, part;  // bit: chunk
+    int hi, lo;
+};
+__device__ __forceinline__ Sight sight(int key0, int pos, int p_min, int p_max, int window) {
+    Sight s;
+    s.none = s.part = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, v + 32 * j);
-    tmem_wait_ld();
-    if (EDGE) mask_half(v, hi, lo), mask_half(v + 64, hi - 64, lo - 64);
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int j = 0; j < 128; j += 8)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[j + 2 * q])), __uint_as_float(v[j + 2 * q + 1]));
-    const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+    for (int x = 0; x < 4; ++x) {
+        const int k = key0 + 32 * x;
+        if (k > p_max || (window && k + 31 <= p_min - window))
+            s.none |= 1u << x;
+        else if (k + 31 > p_min || (window && k <= p_max - window))
+            s.part |= 1u << x;
+    }
+    s.hi = pos - key0;
+    s.lo = window ? s.hi - window : -1;
+    return s;
+}
+
+// Moves the reference m to `top` if some row of the warp has outgrown it, and rescales what refers to it.
+template <int D>
+__device__ __forceinline__ void move_reference(uint32_t to, float c, float top, bool first, float &m, float &l) {
     if (__any_sync(0xffffffffu, (top - m) * c > 8.f)) {  // (false where both are -inf)
         const float f = ex2_approx((m - (top == -INFINITY ? 0.f : top)) * c);
         m = top;
         l *= f;
         if (!first) {
             // the scores are complete: so is the product before them, and O is still
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < D; j += 16) {
                 uint32_t o[16];
                 tmem_ld16(to + j, o);
@@ -166,15 +192,66 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
             }
         }
     }
+}
+
+// One row's scores of a unit (tensor memory, 128 columns at ts) to weights (over them, packed) under the
+// reference m, with their sum added to l.
+template <int D, bool F16>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, bool first, float &m, float &l) {
+    uint32_t v[128];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, v + 32 * x);
+    tmem_wait_ld();
+    move_reference<D>(to, c, fmaxf(fmaxf(fmaxf(max32(v), max32(v + 32)), fmaxf(max32(v + 64), max32(v + 96))), m), first, m, l);
     const float mc = m == -INFINITY ? 0.f : m * c;
-    l += weigh_half<F16>(v, v, c, mc);
-    tmem_st32(ts, v);
-    l += weigh_half<F16>(v + 64, v, c, mc);
-    tmem_st32(ts + 32, v);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        l += weigh<F16>(v + 32 * x, v + 16 * x, c, mc);
+        if (x & 1) tmem_st32(ts + 16 * (x - 1), v + 16 * (x - 1));
+    }
     tmem_wait_st();
     tc_fence_before();
-    __syncwarp();
-    if (lane_id() == 0) mbar_arrive(ready);
+}
+
+// The same where not all is seen: by chunks of 32 keys, of which those that no row of the warp sees cost
+// nothing; the scores are read twice, for the maximum and for the weights.
+template <int D, bool F16>
+__device__ __forceinline__ void softmax_edge(uint32_t ts, uint32_t to, float c, const Sight &see, bool first, float &m,
+                                             float &l) {
+    uint32_t v[32];
+    auto load = [&](int x) {
+        tmem_ld32(ts + 32 * x, v);
+        tmem_wait_ld();
+        if (see.part >> x & 1) {
+            // bit j: key j of the chunk is seen
+            auto upto = [](int n) { return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1; };
+            const uint32_t seen = upto(see.hi - 32 * x) & ~upto(see.lo - 32 * x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = seen & (1u << j) ? v[j] : 0xff800000u;
+        }
+    };
+    float top = m;
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+        if (see.none >> x & 1) continue;
+        load(x);
+        top = fmaxf(top, max32(v));
+    }
+    move_reference<D>(to, c, top, first, m, l);
+    const float mc = m == -INFINITY ? 0.f : m * c;
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {
+        if (see.none >> x & 1) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0;
+        } else {
+            load(x);
+            l += weigh<F16>(v, v, c, mc);
+        }
+        tmem_st16(ts + 16 * x, v);
+    }
+    tmem_wait_st();
+    tc_fence_before();
 }
 
 // Whether a unit of the tile has positions that none of its rows sees.
@@ -197,12 +274,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __shared__ int abort_flag;
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 2), mbar_init(&v_clear[s], 1);
+        for (int s = 0; s < NST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 3), mbar_init(&v_clear[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1), mbar_init(&p_full[s], 4), mbar_init(&o_full[s], 1);
         }
-        mbar_init(&drain, 1);
+        mbar_init(&drain, 2);
         abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
@@ -273,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 ok = __all_sync(0xffffffffu, ok);
                                 if (!ok) break;
                                 if (lane == 0) {
-                                    const int tok = g.s.q0 + (g.x.row0 + st * (p.TM / 2)) / p.G;
+                                    const int tok = g.s.q0 + p.by_G.div(g.x.row0 + st * (p.TM / 2));
                                     mbar_expect_tx(&q_full[st], (p.TM / 2) * 128 * C::NH);
 #pragma unroll
                                     for (int x = 0; x < C::NH; ++x)
@@ -295,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int st = 0; st < 2; ++st)
                     if (qn[st]) mbar_wait(&q_full[st], (qn[st] - 1) & 1, p.err, nullptr);
             }
-        } else if (warp == MMA_WARP) {
+        } else if (warp < MMA_WARP + 2) {
             // ---- matrix products: one thread.  What it does between two products is seen by the tensor pipe (its
             // queue is short), so it does little: descriptors differ in their start address alone (16-byte units
             // in the low bits), ring positions are counted along, and values are cleared by another warp. ----
@@ -305,15 +382,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 constexpr uint32_t ID_PV = idesc(FMT, FMT, 0, 1, D, 128);
                 const uint64_t dq = sdesc(smem_u32(Qs), 16, 1024, SWZ_128B), dk = sdesc(smem_u32(ring), 16, 1024, SWZ_128B),
                                dv = sdesc(smem_u32(ring), C::BLOCK, 1024, SWZ_128B);
+                const int st = warp - MMA_WARP;
+                const uint32_t ta = tmem + st * 128, oa = tmem + C::O_COL + st * 128;
+                const uint64_t dqs = dq + (st * C::TILE >> 4);
                 int slot = 0, vslot = 0;  // ring positions of K(i) and V(i-1), and the parity of their use
-                uint32_t par = 0, vpar = 0, qpar[2] = {0, 0}, ppar[2] = {0, 0}, cpar = 0;
+                uint32_t par = 0, vpar = 0, qpar = 0, ppar = 0, cpar = 0;
                 bool ok = true;
                 auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = mbar_wait(bar, parity, p.err, &abort_flag); };
                 auto advance = [&] {
                     if (++slot == NST) slot = 0, par ^= 1;
                 };
                 while (ok && next_segment<UNIT>(p, cur, g)) {
-                    const Stream s0 = stream_info(p, g, 0), s1 = stream_info(p, g, 1);
+                    const Stream s = stream_info(p, g, st);
                     const int key_u0 = g.x.u0 * UNIT;
                     for (int i = g.u_begin; i <= g.u_end; ++i) {
                         const bool has_s = i < g.u_end, has_pv = i > g.u_begin;
@@ -330,36 +410,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (!wait(&v_clear[vslot], (cpar >> vslot) & 1)) break;
                                 cpar ^= 1u << vslot;
                             }
-                        }
-                        const uint64_t kd = dk + kslot * (C::TILE >> 4), vd = dv + vslot * (C::TILE >> 4);
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            const int lo = st ? s1.lo : s0.lo, hi = st ? s1.hi : s0.hi;
-                            if (has_pv && i - 1 >= lo && i - 1 < hi) {
-                                if (!wait(&p_full[st], ppar[st])) break;
-                                ppar[st] ^= 1;
+                            if (i - 1 >= s.lo && i - 1 < s.hi) {
+                                const uint64_t vd = dv + vslot * (C::TILE >> 4);
+                                if (!wait(&p_full[st], ppar)) break;
+                                ppar ^= 1;
                                 tc_fence_after();
-                                mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128, vd, ID_PV, i - 1 > lo);
+                                mma_ts(oa, ta, vd, ID_PV, i - 1 > s.lo);
 #pragma unroll
-                                for (int k = 1; k < UNIT / 16; ++k)
-                                    mma_ts(tmem + C::O_COL + st * 128, tmem + st * 128 + k * 8, vd + (2048 >> 4) * k, ID_PV, 1);
-                                if (i == hi) mma_commit(&o_full[st]);
-                            }
-                            if (has_s && i >= lo && i < hi) {
-                                if (i == lo) {
-                                    if (!wait(&q_full[st], qpar[st])) break;
-                                    qpar[st] ^= 1;
-                                }
-#pragma unroll
-                                for (int k = 0; k < D / 16; ++k) {
-                                    const uint32_t o = (k >> 2) * C::BLOCK + (k & 3) * 32;
-                                    mma_bf16(tmem + st * 128, dq + ((st * C::TILE + o) >> 4), kd + (o >> 4), ID_S, k > 0);
-                                }
-                                mma_commit(&s_full[st]);
-                                if (i + 1 == hi) mma_commit(&q_empty[st]);
+                                for (int k = 1; k < UNIT / 16; ++k) mma_ts(oa, ta + k * 8, vd + (2048 >> 4) * k, ID_PV, 1);
+                                if (i == s.hi) mma_commit(&o_full[st]);
                             }
                         }
-                        if (!ok) break;
+                        if (has_s && i >= s.lo && i < s.hi) {
+                            const uint64_t kd = dk + kslot * (C::TILE >> 4);
+                            if (i == s.lo) {
+                                if (!wait(&q_full[st], qpar)) break;
+                                qpar ^= 1;
+                            }
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t o = (k >> 2) * C::BLOCK + (k & 3) * 32;
+                                mma_bf16(ta, dqs + (o >> 4), kd + (o >> 4), ID_S, k > 0);
+                            }
+                            mma_commit(&s_full[st]);
+                            if (i + 1 == s.hi) mma_commit(&q_empty[st]);
+                        }
                         if (has_pv) mma_commit(&empty[vslot]);
                         if (has_s) {
                             mma_commit(&empty[kslot]);
@@ -420,11 +495,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t sn = 0, on = 0;  // S tiles and outputs waited for
         bool ok = true;
         // A row of scores needs 128 registers: the walk's state waits in shared memory meanwhile.
+        const int tok = p.by_G.div(r);
         Walk &wk = walk[warp];
         if (lane == 0) wk.cur = cur;
         __syncwarp();
         while (ok) {
-            int i, hi, key0, p_first, p_last, pos;
+            int i, hi, key0, p_first, pos, p_min, p_max;  // (p_min .. p_max: of the warp's rows)
             bool have;
             {
                 Cursor cu = wk.cur;
@@ -433,9 +509,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!more) break;
                 const Stream s = stream_info(p, g, st);
                 have = r < s.rows;
-                const int tok = r / p.G;
                 pos = have ? s.p_first + tok : -1;
-                i = s.lo, hi = s.hi, key0 = (g.x.u0 + s.lo) * UNIT, p_first = s.p_first, p_last = s.p_last;
+                p_min = s.p_first + p.by_G.div(r & ~31), p_max = min(s.p_first + p.by_G.div(r | 31), s.p_last);
+                i = s.lo, hi = s.hi, key0 = (g.x.u0 + s.lo) * UNIT, p_first = s.p_first;
                 if (lane == 0) {
                     wk.cur = cu;
                     wk.end = cu.at - (g.u_end - g.u_begin) + g.x.nu;
@@ -453,12 +529,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 ++sn;
                 tc_fence_after();
-                if (key0 + UNIT - 1 > p_first || (p.window && key0 <= p_last - p.window))
-                    softmax_tile<D, F16, true>(ts, to, c, pos - key0, p.window ? pos - key0 - p.window : -1, first, m, l,
-                                                 &p_full[st]);
+                if (key0 + UNIT - 1 <= p_min && (!p.window || key0 > p_max - p.window))
+                    softmax_tile<D, F16>(ts, to, c, first, m, l);
                 else
-                    softmax_tile<D, F16, false>(ts, to, c, 0, 0, first, m, l,
-                                                 &p_full[st]);
+                    softmax_edge<D, F16>(ts, to, c, sight(key0, pos, p_min, p_max, p.window), first, m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[st]);
             }
             if (!ok) break;
             if (some) {
@@ -471,7 +547,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool whole = wk.whole;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const float ls = l > 0.f ? m * c + log2f(l) : -INFINITY;
-            const int tok = r / p.G;
             const int64_t orow = (int64_t)(wk.row0 + p_first + tok) * p.H + wk.h * p.G + (r - tok * p.G);
             const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + st * (p.TM / 2) + r;
             if (have) {
@@ -480,7 +555,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 else if (p.lse)
                     p.lse[orow] = ls * 0.6931471805599453f;
             }
-#pragma unroll
+            uint16_t *orow_p = static_cast<uint16_t *>(p.out) + orow * D;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll 1
             for (int j = 0; j < D; j += 32) {
                 uint32_t o[32];
                 if (some) {
@@ -491,19 +568,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int q = 0; q < 32; ++q) o[q] = l > 0.f ? __float_as_uint(__uint_as_float(o[q]) * inv) : 0u;
                 if (!have) continue;
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * D + j);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = paged_pack2<F16>(__uint_as_float(o[8 * q + 2 * e]), __uint_as_float(o[8 * q + 2 * e + 1]));
-                        dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int q = 0; q < 16; ++q)
+                        o[q] = paged_pack2<F16>(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1]));
+                    store32(orow_p + j, o, wide), store32(orow_p + j + 16, o + 8, wide);
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + piece * D + j);
+                    float *dst = p.part_o + piece * D + j;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    for (int q = 0; q < 4; ++q) store32(dst + 8 * q, o + 8 * q, true);
                 }
             }
             if (threadIdx.x == 0 && wk.slot == 1 && !whole)

@@ -20,12 +20,25 @@
 
 namespace dsa {
 
+// n / d for 0 <= n < 2^31 by a multiplication: (high(n mul) + n) >> shift, with 2^shift the power of two at or
+// above d and mul = floor(2^32 (2^shift - d) / d) + 1 (divisions by invariant integers, Granlund and Montgomery 1994).
+struct FastDiv {
+    uint32_t mul, shift;
+    static FastDiv of(uint32_t d) {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        return FastDiv{(uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 struct PagedAttnParams {
     const void *q;
     int64_t q_token, q_head;
     const int32_t *q_start;
     PagedDev pg;
-    int32_t T, H, Hkv, G, TM;
+    int32_t T, H, Hkv, G, TM;  // T H < 2^31
+    FastDiv by_G, by_TM;
     int32_t max_q, max_len, window;
     float scale_log2;  // sm_scale * log2(e) (and 1 / k_scale)
     float v_inv;       // 1 / v_scale
@@ -79,8 +92,8 @@ __device__ __forceinline__ Tile tile_info(const PagedAttnParams &p, const SeqInf
     const int total = s.n * p.G;
     x.row0 = t * p.TM;
     x.rows = min(p.TM, total - x.row0);
-    x.p_first = s.L - s.n + x.row0 / p.G;
-    x.p_last = s.L - s.n + (x.row0 + x.rows - 1) / p.G;
+    x.p_first = s.L - s.n + p.by_G.div(x.row0);
+    x.p_last = s.L - s.n + p.by_G.div(x.row0 + x.rows - 1);
     x.key_hi = max(x.p_last + 1, 0);
     x.key_lo = p.window ? max(x.p_first - p.window + 1, 0) : 0;
     x.u0 = x.key_lo / UNIT;
@@ -88,11 +101,29 @@ __device__ __forceinline__ Tile tile_info(const PagedAttnParams &p, const SeqInf
     return x;
 }
 __device__ __forceinline__ int seq_tiles(const PagedAttnParams &p, const SeqInfo &s) {
-    return (int)(((int64_t)s.n * p.G + p.TM - 1) / p.TM);
+    return s.n ? p.by_TM.div(s.n * p.G - 1) + 1 : 0;
 }
 
-// Where on the line CTA c of nc begins.
-__device__ __forceinline__ int64_t line_start(int64_t total, int c, int nc) { return total * c / nc; }
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {  // a >= 0, b > 0; short where both are
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+// The line's parts: the first `more` CTAs have per + 1 units, the others per.
+struct Line {
+    int64_t per;
+    int more;
+    __device__ __forceinline__ Line(int64_t total, int nc) {
+        per = div64(total, nc);
+        more = (int)(total - per * nc);
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return per * c + min(c, more); }
+    // the first CTA that begins at or behind `at`
+    __device__ __forceinline__ int next(int64_t at) const {
+        const int64_t big = (per + 1) * more;
+        if (at <= big) return (int)div64(at + per, per + 1);
+        return more + (int)(per > 0 ? div64(at - big + per - 1, per) : 0);
+    }
+};
 
 struct Cursor {
     int b, h, t, u;   // sequence, K/V head, tile, unit of the tile
@@ -148,7 +179,8 @@ __device__ void plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh
         __syncthreads();
     }
     const int64_t total = sh.total;
-    const int64_t begin = line_start(total, c, nc), end = line_start(total, c + 1, nc);
+    const Line line(total, nc);
+    const int64_t begin = line.start(c), end = line.start(c + 1);
     if (threadIdx.x == 0) sh.cur = Cursor{0, 0, 0, 0, begin, end, total};
     __syncthreads();
     if (begin >= end) return;
@@ -170,7 +202,7 @@ __device__ void plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh
                     const int b = base + g + l;
                     const int64_t per_head = sh.units[g + l];
                     int64_t off = begin - before - __shfl_sync(0xffffffffu, inc - w, l);
-                    const int h = (int)(off / per_head);
+                    const int h = (int)div64(off, per_head);
                     off -= h * per_head;
                     const SeqInfo s = seq_info(p, b);
                     const int nt = seq_tiles(p, s);
