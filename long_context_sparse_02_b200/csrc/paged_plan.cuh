@@ -20,18 +20,6 @@
 
 namespace dsa {
 
-// n / d for 0 <= n < 2^31 by a multiplication: (high(n mul) + n) >> shift, with 2^shift the power of two at or
-// above d and mul = floor(2^32 (2^shift - d) / d) + 1 (divisions by invariant integers, Granlund and Montgomery 1994).
-struct FastDiv {
-    uint32_t mul, shift;
-    static FastDiv of(uint32_t d) {
-        uint32_t s = 0;
-        while ((1ull << s) < d) ++s;
-        return FastDiv{(uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
-    }
-    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
-};
-
 struct PagedAttnParams {
     const void *q;
     int64_t q_token, q_head;

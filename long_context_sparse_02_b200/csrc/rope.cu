@@ -5,11 +5,12 @@
 //
 // The angle is formed in fp64 and reduced to a fraction of a turn in
 // [-1/2, 1/2] before fp32 takes over: at position 2^20 an fp32 angle would be
-// off by up to 0.06 radians.  A block is one token and a run of its heads:
-// its first dim/2 threads take one sine and cosine each into shared memory
-// (shared by all heads), then every thread moves 16-byte vectors, a pair of
-// vectors for a rotated unit.  The first unit's loads are issued before the
-// sines, the page lookup and the barrier, whose latency they hide.
+// off by up to 0.06 radians.  A block is a few tokens (or a part of one token's
+// heads, when there are few tokens): its threads take the sines and cosines
+// into shared memory (shared by all heads of a token) and look up where the
+// tokens go, then move 16-byte vectors, a pair of vectors for a rotated unit,
+// two units of each thread in flight.  The first units' loads are issued
+// before the sines, the page lookup and the barrier, whose latency they hide.
 // HBM-bound: each element is read and written once.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -30,6 +31,7 @@ struct Seg {
     int64_t in_token, in_head, out_token, out_head;  // elements
     int64_t out_page, out_row;                       // paged destinations (paged != 0)
     int32_t heads, D;
+    FastDiv by_units;
     int32_t units;   // per head: rotated ones first, then copied ones
     int32_t rot;     // rotated units per head (0: copied whole)
     int32_t paged, e4m3;
@@ -38,8 +40,11 @@ struct Seg {
 
 struct MoveParams {
     Seg seg[MAX_SEG];
-    int32_t nseg, per_block;  // units per block
-    int32_t total;            // units per token, all segments
+    int32_t nseg, tokens;
+    int32_t per_block;  // tokens per block
+    int32_t part;       // units of each of them that a block moves
+    int32_t total;      // units per token, all segments
+    FastDiv by_part;
     const int32_t *pos, *tok_seq;  // tok_seq NULL: nothing is paged
     PagedDev pg;
     const double *inv_freq;
@@ -137,10 +142,10 @@ __device__ __forceinline__ Unit unit_of(const MoveParams &p, int u) {
         if (r.seg == s && s + 1 < p.nseg && u >= n) u -= n, r.seg = s + 1;
     }
     const Seg &g = p.seg[r.seg];
-    r.head = u / g.units;
+    r.head = g.by_units.div(u);
     const int x = u - r.head * g.units;
     if (x < g.rot) {
-        r.pair = INTER ? x * VEC : x * VEC;
+        r.pair = x * VEC;
         r.e0 = p.offset + (INTER ? 2 * x * VEC : x * VEC);
         r.e1 = INTER ? r.e0 + VEC : r.e0 + p.dim / 2;
     } else {
@@ -151,103 +156,129 @@ __device__ __forceinline__ Unit unit_of(const MoveParams &p, int u) {
     return r;
 }
 
-// cos and sin of the block's token, [dim/2] each, in dynamic shared memory.
+constexpr int MAX_TOKENS = 32;  // per block
+struct Dest {
+    int64_t page;  // -1: nothing is written for the token
+    int row;
+};
+
+// One unit on its way: read by fetch(), turned and written by put().
+template <typename T, int VEC, bool INTER>
+struct Moving {
+    Unit un;
+    int token;  // of the block
+    Vec<T, VEC> a, b;
+
+    __device__ __forceinline__ void fetch(const MoveParams &p, int t0, int u) {
+        token = p.by_part.div(u);
+        un = unit_of<VEC, INTER>(p, blockIdx.y * p.part + u - token * p.part);
+        const Seg &g = p.seg[un.seg];
+        const T *src = static_cast<const T *>(g.in) + (t0 + token) * g.in_token + un.head * g.in_head;
+        a.load(src + un.e0);
+        b.load(src + un.e1);
+    }
+    __device__ __forceinline__ void put(const MoveParams &p, int t0, const float2 *cs_all, const Dest *dest) {
+        const Seg &g = p.seg[un.seg];
+        int64_t at = (int64_t)un.head * g.out_head;
+        if (p.tok_seq) {
+            const Dest d = dest[token];
+            if (d.page < 0) return;
+            if (g.paged) at += d.page * g.out_page + d.row * g.out_row;
+        }
+        if (!g.paged) at += (t0 + token) * g.out_token;
+        if (un.pair < 0 && !g.e4m3) {
+            a.copy(static_cast<T *>(g.out) + at + un.e0);
+            return;
+        }
+        const float2 *cs = cs_all + token * (p.dim / 2) + un.pair;
+        float x[VEC], y[VEC];
+        a.floats(x);
+        b.floats(y);
+        if (un.pair >= 0) {
+            if (INTER && VEC == 1) {
+                const float2 w = cs[0];
+                const float x0 = x[0], y0 = y[0];
+                x[0] = x0 * w.x - y0 * w.y;
+                y[0] = y0 * w.x + x0 * w.y;
+            } else if (INTER) {
+                // pairs lie next to each other: x holds VEC / 2 of them, y the next VEC / 2
+#pragma unroll
+                for (int i = 0; i + 1 < VEC; i += 2) {
+                    const float2 w = cs[i / 2], z = cs[VEC / 2 + i / 2];
+                    const float x0 = x[i], x1 = x[i + 1], y0 = y[i], y1 = y[i + 1];
+                    x[i] = x0 * w.x - x1 * w.y;
+                    x[i + 1] = x1 * w.x + x0 * w.y;
+                    y[i] = y0 * z.x - y1 * z.y;
+                    y[i + 1] = y1 * z.x + y0 * z.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float2 w = cs[i];
+                    const float x0 = x[i], y0 = y[i];
+                    x[i] = x0 * w.x - y0 * w.y;
+                    y[i] = y0 * w.x + x0 * w.y;
+                }
+            }
+        }
+        if (g.e4m3) {
+            uint8_t *o = static_cast<uint8_t *>(g.out) + at;
+            Vec<T, VEC>::store8(o + un.e0, x, g.scale);
+            if (un.pair >= 0) Vec<T, VEC>::store8(o + un.e1, y, g.scale);
+        } else {
+            T *o = static_cast<T *>(g.out) + at;
+            Vec<T, VEC>::store(o + un.e0, x);
+            Vec<T, VEC>::store(o + un.e1, y);
+        }
+    }
+};
+
+// cos and sin of the block's tokens, [tokens][dim/2], in dynamic shared memory.
 template <typename T, int VEC, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS) move_heads_kernel(const __grid_constant__ MoveParams p) {
     extern __shared__ float2 cs[];
-    const int t = blockIdx.x;
-    const int u_end = min(p.total, (int)(blockIdx.y + 1) * p.per_block);
-    int u = blockIdx.y * p.per_block + threadIdx.x;
-    Unit un{};
-    Vec<T, VEC> a, b;
-    auto fetch = [&] {
-        un = unit_of<VEC, INTER>(p, u);
-        const Seg &g = p.seg[un.seg];
-        const T *src = static_cast<const T *>(g.in) + t * g.in_token + un.head * g.in_head;
-        a.load(src + un.e0);
-        b.load(src + un.e1);
-    };
-    if (u < u_end) fetch();
-    const int pos = p.pos[t];
-    int64_t page = 0;
-    int row = 0;
-    bool ok = true;
-    if (p.tok_seq) {
-        const int s = p.tok_seq[t];
-        if (s == -1) return;  // padding (the whole block)
-        uint32_t bad = 0;
-        if (s < 0 || s >= p.pg.num_seqs || pos < 0 || pos >= p.pg.seq_lens[s]) {
-            bad = DSA_DEVERR_POSITION;
-        } else {
-            const int lp = pos >> 6;
-            page = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)s * p.pg.max_blocks + lp] : -1;
-            row = pos & 63;
-            if (page < 0 || page >= p.pg.num_pages) bad = DSA_DEVERR_PAGE;
+    __shared__ Dest dest[MAX_TOKENS];
+    const int t0 = blockIdx.x * p.per_block, nt = min(p.per_block, p.tokens - t0);
+    const int units = nt * min(p.part, p.total - (int)blockIdx.y * p.part);  // (parts are whole, or one token's last)
+    int u = threadIdx.x;
+    Moving<T, VEC, INTER> a, b;
+    if (u < units) a.fetch(p, t0, u);
+    if (u + ROPE_THREADS < units) b.fetch(p, t0, u + ROPE_THREADS);
+    if (p.tok_seq && threadIdx.x < nt) {
+        const int t = t0 + threadIdx.x, s = p.tok_seq[t], pos = p.pos[t];
+        Dest d{-1, 0};
+        if (s != -1) {  // (-1: padding)
+            uint32_t bad = 0;
+            if (s < 0 || s >= p.pg.num_seqs || pos < 0 || pos >= p.pg.seq_lens[s]) {
+                bad = DSA_DEVERR_POSITION;
+            } else {
+                const int lp = pos >> 6;
+                d.page = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)s * p.pg.max_blocks + lp] : -1;
+                d.row = pos & 63;
+                if (d.page < 0 || d.page >= p.pg.num_pages) bad = DSA_DEVERR_PAGE;
+            }
+            if (bad) {
+                d.page = -1;
+                if (blockIdx.y == 0) record_error(p.err, bad);
+            }
         }
-        if (bad) {
-            if (threadIdx.x == 0 && blockIdx.y == 0) record_error(p.err, bad);
-            ok = false;
-        }
+        dest[threadIdx.x] = d;
     }
-    if (!ok) return;  // the same decision in every thread of the block
-    for (int i = threadIdx.x; i < p.dim / 2; i += ROPE_THREADS) {
-        const double turns = (double)pos * p.inv_freq[i] * 0.15915494309189535;  // 1 / 2 pi
+    const int half = p.dim / 2;
+    for (int i = threadIdx.x; i < nt * half; i += ROPE_THREADS) {
+        const int t = i / half;
+        const double turns = (double)p.pos[t0 + t] * p.inv_freq[i - t * half] * 0.15915494309189535;  // 1 / 2 pi
         float sn, c;
         sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
         cs[i] = make_float2(c * p.factor, sn * p.factor * p.sin_sign);
     }
     __syncthreads();
-    while (u < u_end) {
-        const Seg &g = p.seg[un.seg];
-        int64_t at = (int64_t)un.head * g.out_head;
-        at += g.paged ? page * g.out_page + row * g.out_row : t * g.out_token;
-        if (un.pair < 0 && !g.e4m3) {
-            a.copy(static_cast<T *>(g.out) + at + un.e0);
-        } else {
-            float x[VEC], y[VEC];
-            a.floats(x);
-            b.floats(y);
-            if (un.pair >= 0) {
-                if (INTER) {
-                    // pairs lie next to each other: x then y hold VEC pairs (VEC = 1: one pair, x and y)
-#pragma unroll
-                    for (int i = 0; i < VEC; i += 2) {
-                        if (VEC == 1) {
-                            const float2 w = cs[un.pair];
-                            const float x0 = x[0], y0 = y[0];
-                            x[0] = x0 * w.x - y0 * w.y;
-                            y[0] = y0 * w.x + x0 * w.y;
-                        } else {
-                            const float2 w = cs[un.pair + i / 2], z = cs[un.pair + VEC / 2 + i / 2];
-                            const float x0 = x[i], x1 = x[(i + 1) % VEC], y0 = y[i], y1 = y[(i + 1) % VEC];
-                            x[i] = x0 * w.x - x1 * w.y;
-                            x[(i + 1) % VEC] = x1 * w.x + x0 * w.y;
-                            y[i] = y0 * z.x - y1 * z.y;
-                            y[(i + 1) % VEC] = y1 * z.x + y0 * z.y;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float2 w = cs[un.pair + i];
-                        const float x0 = x[i], y0 = y[i];
-                        x[i] = x0 * w.x - y0 * w.y;
-                        y[i] = y0 * w.x + x0 * w.y;
-                    }
-                }
-            }
-            if (g.e4m3) {
-                uint8_t *o = static_cast<uint8_t *>(g.out) + at;
-                Vec<T, VEC>::store8(o + un.e0, x, g.scale);
-                if (un.pair >= 0) Vec<T, VEC>::store8(o + un.e1, y, g.scale);
-            } else {
-                T *o = static_cast<T *>(g.out) + at;
-                Vec<T, VEC>::store(o + un.e0, x);
-                Vec<T, VEC>::store(o + un.e1, y);
-            }
-        }
-        u += ROPE_THREADS;
-        if (u < u_end) fetch();
+    while (u < units) {
+        a.put(p, t0, cs, dest);
+        if (u + ROPE_THREADS < units) b.put(p, t0, cs, dest);
+        u += 2 * ROPE_THREADS;
+        if (u < units) a.fetch(p, t0, u);
+        if (u + ROPE_THREADS < units) b.fetch(p, t0, u + ROPE_THREADS);
     }
 }
 
@@ -260,24 +291,37 @@ dsa_status launch_move(MoveParams &p, int T_tokens, int sm_count, cudaStream_t s
         // heads rotated in place leave their other elements where they are
         const bool still = g.in == g.out && !g.paged && g.rot;
         g.units = g.rot + (still ? 0 : (g.D - (g.rot ? p.dim : 0)) / VEC);
+        g.by_units = FastDiv::of(g.units > 0 ? g.units : 1);
         total += (int64_t)g.heads * g.units;
     }
     if (total == 0 || T_tokens == 0) return DSA_OK;
-    if (total > (1 << 30)) return DSA_ERR_UNSUPPORTED;
+    if (total > (1 << 26)) return DSA_ERR_UNSUPPORTED;
     p.total = (int32_t)total;
-    // One block a token once there are enough tokens; few tokens are split over
-    // their heads until every SM has about two blocks, each of at least one
-    // unit a thread (a decode step of 8 tokens x 128 heads: 34 blocks a token).
-    const int64_t most = (total + ROPE_THREADS - 1) / ROPE_THREADS;
-    int64_t split = (2 * (int64_t)sm_count + T_tokens - 1) / T_tokens;
-    split = split < most ? split : most;
-    if (split > 65535) split = 65535;
-    p.per_block = (int32_t)((total + split - 1) / split);
-    split = (total + p.per_block - 1) / p.per_block;
-    const size_t smem = (size_t)(p.dim / 2) * sizeof(float2);
+    p.tokens = T_tokens;
+    // A block moves about four units a thread: that many tokens, as far as their sines fit (16 KB) and two
+    // blocks an SM remain.  Fewer tokens than that are split over their heads, down to one unit a thread.
+    // (32768 latent rows, 68 units each: 97 us with a block a token.)
+    int64_t per = 4 * ROPE_THREADS / total;
+    const int64_t fit = p.dim ? 4096 / p.dim : MAX_TOKENS, spread = T_tokens / (2 * (int64_t)sm_count);
+    for (const int64_t x : {fit, spread, (int64_t)MAX_TOKENS}) per = x < per ? x : per;
+    p.per_block = per > 1 ? (int32_t)per : 1;
+    int64_t split = 1;
+    if (p.per_block == 1) {
+        const int64_t most = (total + ROPE_THREADS - 1) / ROPE_THREADS;
+        split = (2 * (int64_t)sm_count + T_tokens - 1) / T_tokens;
+        const int64_t full = total / (4 * ROPE_THREADS);  // long tokens: four units a thread here too
+        split = split > full ? split : full;
+        split = split < most ? split : most;
+        split = split < 1 ? 1 : split > 65535 ? 65535 : split;
+    }
+    p.part = (int32_t)((total + split - 1) / split);
+    p.by_part = FastDiv::of(p.part);
+    split = (total + p.part - 1) / p.part;
+    const unsigned blocks = (unsigned)((T_tokens + p.per_block - 1) / p.per_block);
+    const size_t smem = (size_t)p.per_block * (p.dim / 2) * sizeof(float2);
     auto fn = move_heads_kernel<T, VEC, INTER>;
     if (smem > 48 * 1024 && !ensure_smem(reinterpret_cast<const void *>(fn), (int)smem)) return DSA_ERR_UNSUPPORTED;
-    fn<<<dim3(T_tokens, (unsigned)split), ROPE_THREADS, smem, st>>>(p);
+    fn<<<dim3(blocks, (unsigned)split), ROPE_THREADS, smem, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
