@@ -8,9 +8,11 @@
 // off by up to 0.06 radians.  A block is a few tokens (or a part of one token's
 // heads, when there are few tokens): its threads take the sines and cosines
 // into shared memory (shared by all heads of a token) and look up where the
-// tokens go, then move 16-byte vectors, a pair of vectors for a rotated unit,
-// two units of each thread in flight.  The first units' loads are issued
-// before the sines, the page lookup and the barrier, whose latency they hide.
+// tokens go.  A thread keeps its place within a head (a unit: two 16-byte
+// vectors) and goes from head to head, two at a time in flight, so that a
+// unit costs its loads, products and stores and little else.  The first
+// loads are issued before the sines, the page lookup and the barrier, whose
+// latency they hide.
 // HBM-bound: each element is read and written once.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -21,7 +23,7 @@
 namespace dsa {
 namespace {
 
-constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_THREADS = 128;
 constexpr int MAX_SEG = 3;
 
 // One array of heads: where its tokens' heads come from, where they go.
@@ -31,9 +33,10 @@ struct Seg {
     int64_t in_token, in_head, out_token, out_head;  // elements
     int64_t out_page, out_row;                       // paged destinations (paged != 0)
     int32_t heads, D;
-    FastDiv by_units;
-    int32_t units;   // per head: rotated ones first, then copied ones
-    int32_t rot;     // rotated units per head (0: copied whole)
+    int32_t units;  // per head: rotated ones first, then copied ones
+    int32_t rot;    // rotated units per head (0: copied whole)
+    int32_t wide;   // a copied unit is two vectors
+    FastDiv by_units, by_heads;  // (by_units: of the first ROPE_THREADS)
     int32_t paged, e4m3;
     float scale;
 };
@@ -41,10 +44,8 @@ struct Seg {
 struct MoveParams {
     Seg seg[MAX_SEG];
     int32_t nseg, tokens;
-    int32_t per_block;  // tokens per block
-    int32_t part;       // units of each of them that a block moves
-    int32_t total;      // units per token, all segments
-    FastDiv by_part;
+    int32_t per_block;    // tokens per block
+    int32_t heads, part;  // heads of a token, all segments; those that a block moves
     const int32_t *pos, *tok_seq;  // tok_seq NULL: nothing is paged
     PagedDev pg;
     const double *inv_freq;
@@ -125,35 +126,23 @@ struct Vec<T, 1> {
     }
 };
 
-// Where a unit lies: its segment, head and elements.  A rotated unit is two
-// vectors: elements e0.. and e1.. (the pair partners in the half layout,
-// neighbours in the interleaved one); a copied one is the vector at e0.
+// Where a unit lies in its head.  A rotated one is two vectors: elements e0..
+// and e1.. (the pair partners in the half layout, neighbours in the
+// interleaved one); a copied one is two neighbours too, or one where their
+// number is odd or the rotated part begins between two (then e1 = e0).
 struct Unit {
-    int seg, head, e0, e1, pair;  // pair < 0: copied; else the first pair's index
+    int e0, e1;
 };
 
 template <int VEC, bool INTER>
-__device__ __forceinline__ Unit unit_of(const MoveParams &p, int u) {
-    Unit r;
-    r.seg = 0;
-#pragma unroll
-    for (int s = 0; s < MAX_SEG - 1; ++s) {
-        const int n = p.seg[s].heads * p.seg[s].units;
-        if (r.seg == s && s + 1 < p.nseg && u >= n) u -= n, r.seg = s + 1;
-    }
-    const Seg &g = p.seg[r.seg];
-    r.head = g.by_units.div(u);
-    const int x = u - r.head * g.units;
+__device__ __forceinline__ Unit unit_of(const MoveParams &p, const Seg &g, int x) {
     if (x < g.rot) {
-        r.pair = x * VEC;
-        r.e0 = p.offset + (INTER ? 2 * x * VEC : x * VEC);
-        r.e1 = INTER ? r.e0 + VEC : r.e0 + p.dim / 2;
-    } else {
-        int e = (x - g.rot) * VEC;
-        if (g.rot && e >= p.offset) e += p.dim;  // past the rotated part
-        r.pair = -1, r.e0 = e, r.e1 = e;
+        const int e = p.offset + (INTER ? 2 * x * VEC : x * VEC);
+        return Unit{e, INTER ? e + VEC : e + p.dim / 2};
     }
-    return r;
+    int e = (x - g.rot) * (g.wide ? 2 * VEC : VEC);
+    if (g.rot && e >= p.offset) e += p.dim;  // past the rotated part
+    return Unit{e, g.wide ? e + VEC : e};
 }
 
 constexpr int MAX_TOKENS = 32;  // per block
@@ -162,98 +151,146 @@ struct Dest {
     int row;
 };
 
-// One unit on its way: read by fetch(), turned and written by put().
-template <typename T, int VEC, bool INTER>
-struct Moving {
-    Unit un;
-    int token;  // of the block
-    Vec<T, VEC> a, b;
+// The sines and cosines of a unit's VEC pairs, and where they lie in shared memory (of `rot` units a token):
+// pairs 2j, 2j + 1 of neighbouring units next to each other, so that neighbouring threads read neighbouring
+// 16 bytes.
+template <int VEC>
+__device__ __forceinline__ int cs_at(int pair, int rot) {
+    if (VEC == 1) return pair;
+    return ((pair % VEC >> 1) * rot + pair / VEC) * 2 + (pair & 1);
+}
+template <int VEC>
+__device__ __forceinline__ void load_cs(float2 *w, const float2 *cs, int x, int rot) {
+    if (VEC == 1) {
+        w[0] = cs[x];
+    } else {
+#pragma unroll
+        for (int j = 0; j + 1 < VEC; j += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(cs + ((j >> 1) * rot + x) * 2);
+            w[j] = make_float2(v.x, v.y), w[j + 1] = make_float2(v.z, v.w);
+        }
+    }
+}
+__device__ __forceinline__ void turn1(float &a, float &b, float2 w) {
+    const float a0 = a, b0 = b;
+    a = a0 * w.x - b0 * w.y;
+    b = b0 * w.x + a0 * w.y;
+}
+template <int VEC, bool INTER>
+__device__ __forceinline__ void turn(float *x, float *y, const float2 *w) {
+    if (INTER && VEC > 1) {  // pairs lie next to each other: x holds VEC / 2 of them, y the next VEC / 2
+#pragma unroll
+        for (int i = 0; i + 1 < VEC; i += 2) turn1(x[i], x[i + 1], w[i / 2]), turn1(y[i], y[i + 1], w[VEC / 2 + i / 2]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) turn1(x[i], y[i], w[i]);
+    }
+}
 
-    __device__ __forceinline__ void fetch(const MoveParams &p, int t0, int u) {
-        token = p.by_part.div(u);
-        un = unit_of<VEC, INTER>(p, blockIdx.y * p.part + u - token * p.part);
-        const Seg &g = p.seg[un.seg];
-        const T *src = static_cast<const T *>(g.in) + (t0 + token) * g.in_token + un.head * g.in_head;
-        a.load(src + un.e0);
-        b.load(src + un.e1);
-    }
-    __device__ __forceinline__ void put(const MoveParams &p, int t0, const float2 *cs_all, const Dest *dest) {
-        const Seg &g = p.seg[un.seg];
-        int64_t at = (int64_t)un.head * g.out_head;
-        if (p.tok_seq) {
-            const Dest d = dest[token];
-            if (d.page < 0) return;
-            if (g.paged) at += d.page * g.out_page + d.row * g.out_row;
-        }
-        if (!g.paged) at += (t0 + token) * g.out_token;
-        if (un.pair < 0 && !g.e4m3) {
-            a.copy(static_cast<T *>(g.out) + at + un.e0);
-            return;
-        }
-        const float2 *cs = cs_all + token * (p.dim / 2) + un.pair;
-        float x[VEC], y[VEC];
-        a.floats(x);
-        b.floats(y);
-        if (un.pair >= 0) {
-            if (INTER && VEC == 1) {
-                const float2 w = cs[0];
-                const float x0 = x[0], y0 = y[0];
-                x[0] = x0 * w.x - y0 * w.y;
-                y[0] = y0 * w.x + x0 * w.y;
-            } else if (INTER) {
-                // pairs lie next to each other: x holds VEC / 2 of them, y the next VEC / 2
-#pragma unroll
-                for (int i = 0; i + 1 < VEC; i += 2) {
-                    const float2 w = cs[i / 2], z = cs[VEC / 2 + i / 2];
-                    const float x0 = x[i], x1 = x[i + 1], y0 = y[i], y1 = y[i + 1];
-                    x[i] = x0 * w.x - x1 * w.y;
-                    x[i + 1] = x1 * w.x + x0 * w.y;
-                    y[i] = y0 * z.x - y1 * z.y;
-                    y[i + 1] = y1 * z.x + y0 * z.y;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float2 w = cs[i];
-                    const float x0 = x[i], y0 = y[i];
-                    x[i] = x0 * w.x - y0 * w.y;
-                    y[i] = y0 * w.x + x0 * w.y;
-                }
-            }
-        }
-        if (g.e4m3) {
-            uint8_t *o = static_cast<uint8_t *>(g.out) + at;
-            Vec<T, VEC>::store8(o + un.e0, x, g.scale);
-            if (un.pair >= 0) Vec<T, VEC>::store8(o + un.e1, y, g.scale);
-        } else {
-            T *o = static_cast<T *>(g.out) + at;
-            Vec<T, VEC>::store(o + un.e0, x);
-            Vec<T, VEC>::store(o + un.e1, y);
-        }
-    }
-};
+constexpr int BATCH = 2;  // heads of a thread in flight
+constexpr int WORK = 16;  // units of a thread in a block, where there are enough
 
 // cos and sin of the block's tokens, [tokens][dim/2], in dynamic shared memory.
 template <typename T, int VEC, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS) move_heads_kernel(const __grid_constant__ MoveParams p) {
-    extern __shared__ float2 cs[];
+    extern __shared__ __align__(16) float2 cs[];
     __shared__ Dest dest[MAX_TOKENS];
-    const int t0 = blockIdx.x * p.per_block, nt = min(p.per_block, p.tokens - t0);
-    const int units = nt * min(p.part, p.total - (int)blockIdx.y * p.part);  // (parts are whole, or one token's last)
-    int u = threadIdx.x;
-    Moving<T, VEC, INTER> a, b;
-    if (u < units) a.fetch(p, t0, u);
-    if (u + ROPE_THREADS < units) b.fetch(p, t0, u + ROPE_THREADS);
+    const int t0 = blockIdx.x * p.per_block, nt = min(p.per_block, p.tokens - t0), half = p.dim / 2;
+    const int h_begin = blockIdx.y * p.part, h_end = min(h_begin + p.part, p.heads);  // (all heads, or one token's)
+    // this thread's walk: segment s, units x0 .. of its heads; items m (head of a token) from m0, step apart, below n
+    int s = 0, x0 = 0, before = 0, m0 = 0, n = 0, step = 1, lo = 0;
+    int x = 0;  // the unit
+    Unit un{};
+    auto enter = [&] {
+        const Seg &g = p.seg[s];
+        lo = max(h_begin - before, 0);
+        const int nh = min(h_end - before, g.heads) - lo;
+        const int ux = min(g.units - x0, ROPE_THREADS);
+        const int hl = ux == ROPE_THREADS ? 0 : x0 ? threadIdx.x / ux : g.by_units.div(threadIdx.x);
+        step = ux == ROPE_THREADS ? 1 : x0 ? ROPE_THREADS / ux : g.by_units.div(ROPE_THREADS);
+        x = x0 + threadIdx.x - hl * ux;
+        un = unit_of<VEC, INTER>(p, g, x);
+        m0 = hl;
+        n = nh > 0 && hl < step ? nt * nh : 0;
+    };
+    Vec<T, VEC> a[BATCH], b[BATCH];
+    auto token_of = [&](const Seg &g, int m) { return nt == 1 ? 0 : g.by_heads.div(m); };
+    auto fetch = [&] {
+        const Seg &g = p.seg[s];
+        const T *in = static_cast<const T *>(g.in) + t0 * g.in_token;
+        const bool two = un.e1 != un.e0;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int m = m0 + k * step;
+            if (m >= n) break;
+            const int t = token_of(g, m);
+            const T *src = in + t * g.in_token + (m - t * g.heads + lo) * g.in_head;
+            a[k].load(src + un.e0);
+            if (two) b[k].load(src + un.e1);
+        }
+    };
+    auto put = [&] {
+        const Seg &g = p.seg[s];
+        const bool two = un.e1 != un.e0;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int m = m0 + k * step;
+            if (m >= n) break;
+            const int t = token_of(g, m);
+            int64_t at = (m - t * g.heads + lo) * g.out_head;
+            if (p.tok_seq) {
+                const Dest d = dest[t];
+                if (d.page < 0) continue;
+                if (g.paged) at += d.page * g.out_page + d.row * g.out_row;
+            }
+            if (!g.paged) at += (int64_t)(t0 + t) * g.out_token;
+            if (x >= g.rot && !g.e4m3) {
+                T *o = static_cast<T *>(g.out) + at;
+                a[k].copy(o + un.e0);
+                if (two) b[k].copy(o + un.e1);
+                continue;
+            }
+            float f[VEC], h[VEC];
+            a[k].floats(f);
+            b[k].floats(h);
+            if (x < g.rot) {
+                float2 w[VEC];
+                load_cs<VEC>(w, cs + t * half, x, g.rot);
+                turn<VEC, INTER>(f, h, w);
+            }
+            if (g.e4m3) {
+                uint8_t *o = static_cast<uint8_t *>(g.out) + at;
+                Vec<T, VEC>::store8(o + un.e0, f, g.scale);
+                if (two) Vec<T, VEC>::store8(o + un.e1, h, g.scale);
+            } else {
+                T *o = static_cast<T *>(g.out) + at;
+                Vec<T, VEC>::store(o + un.e0, f);
+                Vec<T, VEC>::store(o + un.e1, h);
+            }
+        }
+    };
+    // to the next segment (or run of units of this one) that has something for this thread
+    auto next = [&] {
+        while (s < p.nseg) {
+            enter();
+            if (n > m0) return true;
+            x0 += ROPE_THREADS;
+            if (x0 >= p.seg[s].units) before += p.seg[s].heads, ++s, x0 = 0;
+        }
+        return false;
+    };
+    bool more = next();
+    if (more) fetch();
     if (p.tok_seq && threadIdx.x < nt) {
-        const int t = t0 + threadIdx.x, s = p.tok_seq[t], pos = p.pos[t];
+        const int t = t0 + threadIdx.x, sq = p.tok_seq[t], pos = p.pos[t];
         Dest d{-1, 0};
-        if (s != -1) {  // (-1: padding)
+        if (sq != -1) {  // (-1: padding)
             uint32_t bad = 0;
-            if (s < 0 || s >= p.pg.num_seqs || pos < 0 || pos >= p.pg.seq_lens[s]) {
+            if (sq < 0 || sq >= p.pg.num_seqs || pos < 0 || pos >= p.pg.seq_lens[sq]) {
                 bad = DSA_DEVERR_POSITION;
             } else {
                 const int lp = pos >> 6;
-                d.page = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)s * p.pg.max_blocks + lp] : -1;
+                d.page = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)sq * p.pg.max_blocks + lp] : -1;
                 d.row = pos & 63;
                 if (d.page < 0 || d.page >= p.pg.num_pages) bad = DSA_DEVERR_PAGE;
             }
@@ -264,44 +301,52 @@ __global__ void __launch_bounds__(ROPE_THREADS) move_heads_kernel(const __grid_c
         }
         dest[threadIdx.x] = d;
     }
-    const int half = p.dim / 2;
     for (int i = threadIdx.x; i < nt * half; i += ROPE_THREADS) {
-        const int t = i / half;
+        const int t = nt == 1 ? 0 : i / half;
         const double turns = (double)p.pos[t0 + t] * p.inv_freq[i - t * half] * 0.15915494309189535;  // 1 / 2 pi
         float sn, c;
         sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
-        cs[i] = make_float2(c * p.factor, sn * p.factor * p.sin_sign);
+        const int pair = i - t * half;
+        cs[t * half + cs_at<VEC>(pair, half / VEC)] = make_float2(c * p.factor, sn * p.factor * p.sin_sign);
     }
     __syncthreads();
-    while (u < units) {
-        a.put(p, t0, cs, dest);
-        if (u + ROPE_THREADS < units) b.put(p, t0, cs, dest);
-        u += 2 * ROPE_THREADS;
-        if (u < units) a.fetch(p, t0, u);
-        if (u + ROPE_THREADS < units) b.fetch(p, t0, u + ROPE_THREADS);
+    while (more) {
+        put();
+        m0 += BATCH * step;
+        if (m0 >= n) {
+            x0 += ROPE_THREADS;
+            if (x0 >= p.seg[s].units) before += p.seg[s].heads, ++s, x0 = 0;
+            more = next();
+        }
+        if (more) fetch();
     }
 }
 
 template <typename T, int VEC, bool INTER>
 dsa_status launch_move(MoveParams &p, int T_tokens, int sm_count, cudaStream_t st) {
-    int64_t total = 0;
+    int64_t total = 0, heads = 0;
     for (int s = 0; s < p.nseg; ++s) {
         Seg &g = p.seg[s];
         g.rot = g.rot ? p.dim / (2 * VEC) : 0;
         // heads rotated in place leave their other elements where they are
         const bool still = g.in == g.out && !g.paged && g.rot;
-        g.units = g.rot + (still ? 0 : (g.D - (g.rot ? p.dim : 0)) / VEC);
-        g.by_units = FastDiv::of(g.units > 0 ? g.units : 1);
+        const int copied = still ? 0 : (g.D - (g.rot ? p.dim : 0)) / VEC;
+        g.wide = copied % 2 == 0 && (!g.rot || p.offset % (2 * VEC) == 0);
+        g.units = g.rot + (g.wide ? copied / 2 : copied);
+        g.by_units = FastDiv::of(g.units < ROPE_THREADS ? g.units : ROPE_THREADS);
+        g.by_heads = FastDiv::of(g.heads);
         total += (int64_t)g.heads * g.units;
+        heads += g.heads;
     }
     if (total == 0 || T_tokens == 0) return DSA_OK;
     if (total > (1 << 26)) return DSA_ERR_UNSUPPORTED;
-    p.total = (int32_t)total;
+    p.heads = (int32_t)heads;
     p.tokens = T_tokens;
-    // A block moves about four units a thread: that many tokens, as far as their sines fit (16 KB) and two
-    // blocks an SM remain.  Fewer tokens than that are split over their heads, down to one unit a thread.
-    // (32768 latent rows, 68 units each: 97 us with a block a token.)
-    int64_t per = 4 * ROPE_THREADS / total;
+    // A block moves about WORK units a thread, which pays for its start, sines and barrier: that many tokens,
+    // as far as their sines fit (16 KB) and two blocks an SM remain.  Fewer tokens than that are split over
+    // their heads, down to one unit a thread.  Measured: 16384 tokens of 128 heads of 128 at 16, 8 and 4 units
+    // a thread 168, 175 and 192 us; 32768 latent rows 21 us, at a block a token 97 us.
+    int64_t per = WORK * ROPE_THREADS / total;
     const int64_t fit = p.dim ? 4096 / p.dim : MAX_TOKENS, spread = T_tokens / (2 * (int64_t)sm_count);
     for (const int64_t x : {fit, spread, (int64_t)MAX_TOKENS}) per = x < per ? x : per;
     p.per_block = per > 1 ? (int32_t)per : 1;
@@ -309,14 +354,14 @@ dsa_status launch_move(MoveParams &p, int T_tokens, int sm_count, cudaStream_t s
     if (p.per_block == 1) {
         const int64_t most = (total + ROPE_THREADS - 1) / ROPE_THREADS;
         split = (2 * (int64_t)sm_count + T_tokens - 1) / T_tokens;
-        const int64_t full = total / (4 * ROPE_THREADS);  // long tokens: four units a thread here too
+        const int64_t full = total / (WORK * ROPE_THREADS);  // long tokens: WORK units a thread here too
         split = split > full ? split : full;
         split = split < most ? split : most;
+        split = split < heads ? split : heads;
         split = split < 1 ? 1 : split > 65535 ? 65535 : split;
     }
-    p.part = (int32_t)((total + split - 1) / split);
-    p.by_part = FastDiv::of(p.part);
-    split = (total + p.part - 1) / p.part;
+    p.part = (int32_t)((heads + split - 1) / split);
+    split = (heads + p.part - 1) / p.part;
     const unsigned blocks = (unsigned)((T_tokens + p.per_block - 1) / p.per_block);
     const size_t smem = (size_t)p.per_block * (p.dim / 2) * sizeof(float2);
     auto fn = move_heads_kernel<T, VEC, INTER>;
