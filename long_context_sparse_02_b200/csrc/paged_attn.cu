@@ -9,9 +9,9 @@
 // With few rows the bound is HBM: a K/V head's keys and values are read once
 // for all its query heads (rows are packed: see paged_plan.cuh).  One CTA per
 // SM: a producer warp keeps a ring of units (64 positions = one page, K and V)
-// full by TMA, 160 KB in flight per SM; eight consumer warps take 16-key
-// slices in turn, each with the running statistics and the output of its 16
-// rows in registers, and join at the end of a tile in a fixed order.  Keys
+// full by TMA, 160 KB in flight per SM; eight consumer warps take slices of 32
+// or 16 keys in turn, each with the running statistics and the output of its
+// 16 rows in registers, and join at the end of a tile in a fixed order.  Keys
 // and values go from swizzled shared memory to the fragments by ldmatrix; an
 // 8-bit cache is widened to fp16 (exact) in registers, one conversion for two
 // values, and the rows of q are scaled by a power of two to fit fp16 exactly.
@@ -26,7 +26,10 @@ namespace {
 
 constexpr int UNIT = 64;
 constexpr int CW = 8;  // consumer warps
-constexpr int THREADS = (CW + 1) * 32;
+constexpr int THREADS = (CW + 4) * 32;  // and a warpgroup of which one warp loads
+// registers: 384 x 168 at launch; the roles' shares add up to the same
+constexpr int REG_LAUNCH = 168, REG_CONSUME = 216, REG_LOAD = 72;
+static_assert(CW * 32 * REG_CONSUME + 128 * REG_LOAD == THREADS * REG_LAUNCH, "register shares");
 constexpr int RING_BYTES = 160 * 1024;
 constexpr int MERGE_LD = 4;  // floats of padding per merged row
 
@@ -93,11 +96,11 @@ __device__ __forceinline__ uint32_t widen(uint32_t v) {
 }
 
 // MT = TM / 16 row groups of 16; the consumer warps are MT row groups x CW/MT
-// key slots.  A unit has four 16-key slices; slot s of a row group takes
-// every (CW/MT)-th slice of the run of units.
+// key slots.  A unit has 64 / KW slices of KW keys; where a row group has more
+// slots than that, they take turns unit by unit.
 // IO_F16: q and out are fp16 (else bf16).  The matrix products run in fp16
 // when IO_F16 or the cache is E4M3.
-template <int D, bool IO_F16, bool E4M3>
+template <int D, bool IO_F16, bool E4M3, int KW>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const PagedAttnParams p, const int MT) {
@@ -111,7 +114,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     __shared__ uint64_t full[C::NST], empty[C::NST];
     __shared__ int abort_flag;
     const int warp = warp_id(), lane = lane_id();
+    constexpr int SPU = UNIT / KW, NT = KW / 8;  // slices of a unit, 8-key tiles of a slice
     const int nslot = CW / MT;
+    const int turns = nslot > SPU ? nslot / SPU : 1;  // units in turn (a power of two)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NST; ++s) {
             mbar_init(&full[s], 1);
@@ -128,7 +133,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     Cursor cur = plan.cur;
     Segment g;
 
-    if (warp == CW) {
+    if (warp >= CW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOAD));
+        if (warp != CW) return;
         // ---- producer: one unit = one page, K and V of one head ----
         uint32_t it = 0;
         bool ok = true;
@@ -177,6 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 
     // ---- consumers ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_CONSUME));
     const int rg = warp % MT, slot = warp / MT;
     const int gid = lane >> 2, tig = lane & 3;
     uint32_t it = 0;
@@ -240,100 +248,115 @@ __global__ void __launch_bounds__(THREADS, 1)
 
         auto slice = [&](const uint8_t *st, int key0, int sl) {
             const uint32_t kb = smem_u32(st), vb = kb + C::TILE_BYTES;
-            float s[2][4];
+            float s[NT][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
             if (!E4M3) {
-                const int row = sl * 16 + ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
+                const int row = sl * KW + ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4];
-                    ldsm4(b, kb + tile_off<C::BOX_BYTES>(row, 2 * k + ch));
-                    mma16816<MM_F16>(s[0], qf[k], b[0], b[1]);
-                    mma16816<MM_F16>(s[1], qf[k], b[2], b[3]);
-                }
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int i = 0; i < NT; i += 2) {
+                        uint32_t b[4];
+                        ldsm4(b, kb + tile_off<C::BOX_BYTES>(row + i * 8, 2 * k + ch));
+                        mma16816<MM_F16>(s[i], qf[k], b[0], b[1]);
+                        mma16816<MM_F16>(s[i + 1], qf[k], b[2], b[3]);
+                    }
             } else {
-                const int row = sl * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
+                const int row = sl * KW + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
 #pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    uint32_t b[4];
-                    ldsm4(b, kb + tile_off<C::BOX_BYTES>(row, k + ch));
-                    mma16816<true>(s[0], qf[k], widen(b[0]), widen(b[0] >> 16));
-                    mma16816<true>(s[1], qf[k], widen(b[1]), widen(b[1] >> 16));
-                    mma16816<true>(s[0], qf[k + 1], widen(b[2]), widen(b[2] >> 16));
-                    mma16816<true>(s[1], qf[k + 1], widen(b[3]), widen(b[3] >> 16));
-                }
+                for (int k = 0; k < KS; k += 2)
+#pragma unroll
+                    for (int i = 0; i < NT; i += 2) {
+                        uint32_t b[4];
+                        ldsm4(b, kb + tile_off<C::BOX_BYTES>(row + i * 8, k + ch));
+                        mma16816<true>(s[i], qf[k], widen(b[0]), widen(b[0] >> 16));
+                        mma16816<true>(s[i + 1], qf[k], widen(b[1]), widen(b[1] >> 16));
+                        mma16816<true>(s[i], qf[k + 1], widen(b[2]), widen(b[2] >> 16));
+                        mma16816<true>(s[i + 1], qf[k + 1], widen(b[3]), widen(b[3] >> 16));
+                    }
             }
             // scores in log2 units; masked where a row does not see the key
-            const bool edge = key0 + 15 > g.x.p_first || (p.window && key0 <= g.x.p_last - p.window);
+            const bool edge = key0 + KW - 1 > g.x.p_first || (p.window && key0 <= g.x.p_last - p.window);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = e >> 1;
-                    s[i][e] *= c[r];
-                    if (edge) {
-                        const int key = key0 + i * 8 + tig * 2 + (e & 1);
+                for (int e = 0; e < 4; ++e) s[i][e] *= c[e >> 1];
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + i * 8 + tig * 2 + (e & 1), r = e >> 1;
                         if (key > pos[r] || (p.window && key <= pos[r] - p.window)) s[i][e] = -INFINITY;
                     }
-                }
+            }
             float f[2], mu[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                float x = m[r];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) x = fmaxf(x, fmaxf(s[i][2 * r], s[i][2 * r + 1]));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                x = fmaxf(x, m[r]);
                 mu[r] = x == -INFINITY ? 0.f : x;
                 f[r] = ex2_approx(m[r] - mu[r]);
                 m[r] = x;
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[i][e] = ex2_approx(s[i][e] - mu[e >> 1]);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                l[r] = l[r] * f[r] + ((s[0][2 * r] + s[0][2 * r + 1]) + (s[1][2 * r] + s[1][2 * r + 1]));
+            for (int r = 0; r < 2; ++r) {
+                float x = 0.f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) x += s[i][2 * r] + s[i][2 * r + 1];
+                l[r] = l[r] * f[r] + x;
+            }
             if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll
                 for (int i = 0; i < 2 * KS; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
             }
-            // weights rounded to the values' type for the second product (their sum l is of the unrounded ones)
-            const uint32_t a[4] = {paged_pack2<MM_F16>(s[0][0], s[0][1]), paged_pack2<MM_F16>(s[0][2], s[0][3]),
-                                   paged_pack2<MM_F16>(s[1][0], s[1][1]), paged_pack2<MM_F16>(s[1][2], s[1][3])};
             // values at positions that no row of the tile sees may be anything (unwritten rows): taken as 0
-            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-            const bool clear = key0 + 16 > g.x.key_hi || key0 < g.x.key_lo;
-            if (clear) {
-                auto seen = [&](int k) { return k >= g.x.key_lo && k < g.x.key_hi; };
-                const int k = key0 + tig * 2;
-                keep0 = (seen(k) ? 0xffffu : 0u) | (seen(k + 1) ? 0xffff0000u : 0u);
-                keep1 = (seen(k + 8) ? 0xffffu : 0u) | (seen(k + 9) ? 0xffff0000u : 0u);
-            }
-            const int row = sl * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
-            if (!E4M3) {
+            const bool clear = key0 + KW > g.x.key_hi || key0 < g.x.key_lo;
+            const int row = sl * KW + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
 #pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    uint32_t b[4];
-                    ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row, 2 * j + ch));
-                    mma16816<MM_F16>(o[2 * j], a, b[0] & keep0, b[1] & keep1);
-                    mma16816<MM_F16>(o[2 * j + 1], a, b[2] & keep0, b[3] & keep1);
+            for (int i = 0; i < NT; i += 2) {  // 16 keys
+                // weights rounded to the values' type for the second product (their sum l is of the unrounded ones)
+                const uint32_t a[4] = {paged_pack2<MM_F16>(s[i][0], s[i][1]), paged_pack2<MM_F16>(s[i][2], s[i][3]),
+                                       paged_pack2<MM_F16>(s[i + 1][0], s[i + 1][1]),
+                                       paged_pack2<MM_F16>(s[i + 1][2], s[i + 1][3])};
+                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                if (clear) {
+                    auto seen = [&](int k) { return k >= g.x.key_lo && k < g.x.key_hi; };
+                    const int k = key0 + i * 8 + tig * 2;
+                    keep0 = (seen(k) ? 0xffffu : 0u) | (seen(k + 1) ? 0xffff0000u : 0u);
+                    keep1 = (seen(k + 8) ? 0xffffu : 0u) | (seen(k + 9) ? 0xffff0000u : 0u);
                 }
-            } else {
-                // a transposed 16-bit element is two neighbouring elements of one row: o[2j] takes the
-                // even ones of 16, o[2j + 1] the odd ones
+                if (!E4M3) {
 #pragma unroll
-                for (int j = 0; j < KS; j += 2) {
-                    uint32_t b[4];
-                    ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row, j + ch));
+                    for (int j = 0; j < KS; ++j) {
+                        uint32_t b[4];
+                        ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row + i * 8, 2 * j + ch));
+                        mma16816<MM_F16>(o[2 * j], a, b[0] & keep0, b[1] & keep1);
+                        mma16816<MM_F16>(o[2 * j + 1], a, b[2] & keep0, b[3] & keep1);
+                    }
+                } else {
+                    // a transposed 16-bit element is two neighbouring elements of one row: o[2j] takes the
+                    // even ones of 16, o[2j + 1] the odd ones
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t b0 = b[2 * x], b1 = b[2 * x + 1];
-                        mma16816<true>(o[2 * (j + x)], a, widen(__byte_perm(b0, 0, 0x4420)) & keep0,
-                                       widen(__byte_perm(b1, 0, 0x4420)) & keep1);
-                        mma16816<true>(o[2 * (j + x) + 1], a, widen(__byte_perm(b0, 0, 0x4431)) & keep0,
-                                       widen(__byte_perm(b1, 0, 0x4431)) & keep1);
+                    for (int j = 0; j < KS; j += 2) {
+                        uint32_t b[4];
+                        ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row + i * 8, j + ch));
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t b0 = b[2 * x], b1 = b[2 * x + 1];
+                            mma16816<true>(o[2 * (j + x)], a, widen(__byte_perm(b0, 0, 0x4420)) & keep0,
+                                           widen(__byte_perm(b1, 0, 0x4420)) & keep1);
+                            mma16816<true>(o[2 * (j + x) + 1], a, widen(__byte_perm(b0, 0, 0x4431)) & keep0,
+                                           widen(__byte_perm(b1, 0, 0x4431)) & keep1);
+                        }
                     }
                 }
             }
@@ -341,16 +364,15 @@ __global__ void __launch_bounds__(THREADS, 1)
 
         bool ok = true;
         for (int u = g.u_begin; ok && u < g.u_end; ++u, ++it) {
-            // Every warp waits for and releases every unit, also the ones that the other half of eight slots
-            // takes: a warp that skipped a stage's phase could not tell the one after next by its parity.
+            // Every warp waits for and releases every unit, also the ones that other slots take: a warp that skipped a stage's phase could not tell the one after next by its parity.
             const int s = it % C::NST;
             ok = mbar_wait(&full[s], (it / C::NST) & 1, p.err, &abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t *st = ring + s * C::STAGE;
             const int key0 = (g.x.u0 + u) * UNIT;
-            if (nslot <= 4 || (slot >> 2) == (int)(it & 1))
-                for (int sl = slot & 3; sl < 4; sl += nslot > 4 ? 4 : nslot) slice(st, key0 + sl * 16, sl);
+            if ((slot / SPU & (turns - 1)) == (int)(it & (turns - 1)))
+                for (int sl = slot % SPU; sl < SPU; sl += nslot) slice(st, key0 + sl * KW, sl);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         }
@@ -574,15 +596,28 @@ bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int p
                         inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int D, bool IO_F16, bool E4M3>
-dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
-    auto fn = paged_attn_kernel<D, IO_F16, E4M3>;
+template <int D, bool IO_F16, bool E4M3, int KW>
+dsa_status launch_kw(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    auto fn = paged_attn_kernel<D, IO_F16, E4M3, KW>;
     constexpr int SMEM = Cfg<D, E4M3>::SMEM;
-    if (!ensure_smem(reinterpret_cast<const void *>(fn), SMEM)) return DSA_ERR_CUDA;
+    // the roles' register shares draw on what the block was launched with
+    static const bool regs_ok = [fn] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, fn) == cudaSuccess && fa.numRegs == REG_LAUNCH;
+    }();
+    if (!regs_ok || !ensure_smem(reinterpret_cast<const void *>(fn), SMEM)) return DSA_ERR_CUDA;
     CUtensorMap km, vm;
     if (!paged_kv_maps(*a.cache, a.pg.num_pages, &km, &vm)) return DSA_ERR_CUDA;
     fn<<<nc, THREADS, SMEM, st>>>(km, vm, p, p.TM / 16);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+// Slices of 32 keys, twice as many independent products and half as many exchanges a key as of 16; but where one
+// row group's eight slots would then hold four units of a five-unit ring (16 rows, 2-byte cache, D = 128), 16.
+template <int D, bool IO_F16, bool E4M3>
+dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    if constexpr (Cfg<D, E4M3>::NST < 8)
+        if (p.TM == 16) return launch_kw<D, IO_F16, E4M3, 16>(a, p, nc, st);
+    return launch_kw<D, IO_F16, E4M3, 32>(a, p, nc, st);
 }
 
 template <int D, bool IO_F16>
