@@ -106,7 +106,7 @@ bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, cons
 }
 
 bool make_tmap_4d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, const uint64_t dims[4],
-                  const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle swz) {
+                  const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle swz, int l2_bytes) {
     CUtensorMap probe;
     if (!make_tmap_2d(&probe, base, dt, dims[0], dims[1], strides[0], box[0], box[1], swz)) return false;  // loads the encoder
     cuuint64_t d[4], st[3];
@@ -115,7 +115,9 @@ bool make_tmap_4d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, cons
     for (int i = 0; i < 3; ++i) st[i] = strides[i];
     if (dims[2] == 0 || dims[3] == 0) return false;
     return g_encode(m, dt, 4, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                    l2_bytes >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                    : l2_bytes >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_64B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace dsa

@@ -33,9 +33,10 @@ bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, cons
 
 // Builds a 4-D tiled tensor map: dims[0] elements innermost, then dims[1..3]
 // `strides[0..2]` bytes apart (each a multiple of 16); box[0..3].  Reads
-// outside the dimensions fill with zeros.
+// outside the dimensions fill with zeros.  L2 fetches up to `l2_bytes` (64,
+// 128 or 256) at a time: no more than what lies together and is needed.
 bool make_tmap_4d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, const uint64_t dims[4],
-                  const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle swz);
+                  const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle swz, int l2_bytes);
 
 // Raises the dynamic shared-memory limit of `fn` once per device.
 bool ensure_smem(const void *fn, int bytes);

@@ -41,7 +41,9 @@ struct Cfg {
     static constexpr int BOXES = ROW_BYTES / BOX_BYTES;
     static constexpr int TILE_BYTES = UNIT * ROW_BYTES;                   // K or V of a unit
     static constexpr int STAGE = 2 * TILE_BYTES;
-    static constexpr int NST = RING_BYTES / STAGE < 10 ? RING_BYTES / STAGE : 10;
+    // 128 KB of units, a power of two of them; of the largest ones as many as fit
+    static constexpr int NST = STAGE == 32 * 1024 ? 5 : 128 * 1024 / STAGE;
+    static_assert(NST * STAGE <= RING_BYTES, "ring");
     static constexpr int MERGE_ROW = D + MERGE_LD;
     static constexpr int MERGE_BYTES = (CW / 2) * 16 * (MERGE_ROW + 2) * 4;
     static constexpr int SMEM = NST * STAGE + MERGE_BYTES + 1024;
@@ -88,6 +90,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     if (F16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
+
 // Two e4m3 codes (bits 0-15) to fp16 (exact).
 __device__ __forceinline__ uint32_t widen(uint32_t v) {
     uint32_t r;
@@ -117,10 +124,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int SPU = UNIT / KW, NT = KW / 8;  // slices of a unit, 8-key tiles of a slice
     const int nslot = CW / MT;
     const int turns = nslot > SPU ? nslot / SPU : 1;  // units in turn (a power of two)
+    // Where the ring holds a multiple of them, a stage always belongs to the same slots, and the others pass it by.
+    // Else every warp waits for and releases every unit: one that skipped a stage's phase could not tell the one
+    // after next by its parity.
+    const bool own = C::NST % turns == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NST; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], CW);
+            mbar_init(&empty[s], own ? CW / turns : CW);
         }
         abort_flag = 0;
         fence_mbar_init();
@@ -319,59 +330,66 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 2 * KS; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
             }
             // values at positions that no row of the tile sees may be anything (unwritten rows): taken as 0
-            const bool clear = key0 + KW > g.x.key_hi || key0 < g.x.key_lo;
             const int row = sl * KW + (((lane >> 3) & 1) << 3) + (lane & 7), ch = lane >> 4;
+            auto values = [&](auto clear) {
+                constexpr bool CLEAR = decltype(clear)::value;
 #pragma unroll
-            for (int i = 0; i < NT; i += 2) {  // 16 keys
-                // weights rounded to the values' type for the second product (their sum l is of the unrounded ones)
-                const uint32_t a[4] = {paged_pack2<MM_F16>(s[i][0], s[i][1]), paged_pack2<MM_F16>(s[i][2], s[i][3]),
-                                       paged_pack2<MM_F16>(s[i + 1][0], s[i + 1][1]),
-                                       paged_pack2<MM_F16>(s[i + 1][2], s[i + 1][3])};
-                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-                if (clear) {
-                    auto seen = [&](int k) { return k >= g.x.key_lo && k < g.x.key_hi; };
-                    const int k = key0 + i * 8 + tig * 2;
-                    keep0 = (seen(k) ? 0xffffu : 0u) | (seen(k + 1) ? 0xffff0000u : 0u);
-                    keep1 = (seen(k + 8) ? 0xffffu : 0u) | (seen(k + 9) ? 0xffff0000u : 0u);
-                }
-                if (!E4M3) {
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) {
-                        uint32_t b[4];
-                        ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row + i * 8, 2 * j + ch));
-                        mma16816<MM_F16>(o[2 * j], a, b[0] & keep0, b[1] & keep1);
-                        mma16816<MM_F16>(o[2 * j + 1], a, b[2] & keep0, b[3] & keep1);
+                for (int i = 0; i < NT; i += 2) {  // 16 keys
+                    // weights rounded to the values' type for the second product (their sum l is of the unrounded ones)
+                    const uint32_t a[4] = {paged_pack2<MM_F16>(s[i][0], s[i][1]), paged_pack2<MM_F16>(s[i][2], s[i][3]),
+                                           paged_pack2<MM_F16>(s[i + 1][0], s[i + 1][1]),
+                                           paged_pack2<MM_F16>(s[i + 1][2], s[i + 1][3])};
+                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    if (CLEAR) {
+                        auto seen = [&](int k) { return k >= g.x.key_lo && k < g.x.key_hi; };
+                        const int k = key0 + i * 8 + tig * 2;
+                        keep0 = (seen(k) ? 0xffffu : 0u) | (seen(k + 1) ? 0xffff0000u : 0u);
+                        keep1 = (seen(k + 8) ? 0xffffu : 0u) | (seen(k + 9) ? 0xffff0000u : 0u);
                     }
-                } else {
-                    // a transposed 16-bit element is two neighbouring elements of one row: o[2j] takes the
-                    // even ones of 16, o[2j + 1] the odd ones
+                    if (!E4M3) {
 #pragma unroll
-                    for (int j = 0; j < KS; j += 2) {
-                        uint32_t b[4];
-                        ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row + i * 8, j + ch));
+                        for (int j = 0; j < KS; ++j) {
+                            uint32_t b[4];
+                            ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row + i * 8, 2 * j + ch));
+                            mma16816<MM_F16>(o[2 * j], a, b[0] & keep0, b[1] & keep1);
+                            mma16816<MM_F16>(o[2 * j + 1], a, b[2] & keep0, b[3] & keep1);
+                        }
+                    } else {
+                        // a transposed 16-bit element is two neighbouring elements of one row: o[2j] takes the
+                        // even ones of 16, o[2j + 1] the odd ones
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t b0 = b[2 * x], b1 = b[2 * x + 1];
-                            mma16816<true>(o[2 * (j + x)], a, widen(__byte_perm(b0, 0, 0x4420)) & keep0,
-                                           widen(__byte_perm(b1, 0, 0x4420)) & keep1);
-                            mma16816<true>(o[2 * (j + x) + 1], a, widen(__byte_perm(b0, 0, 0x4431)) & keep0,
-                                           widen(__byte_perm(b1, 0, 0x4431)) & keep1);
+                        for (int j = 0; j < KS; j += 2) {
+                            uint32_t b[4];
+                            ldsm4_t(b, vb + tile_off<C::BOX_BYTES>(row + i * 8, j + ch));
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t b0 = b[2 * x], b1 = b[2 * x + 1];
+                                mma16816<true>(o[2 * (j + x)], a, widen(__byte_perm(b0, 0, 0x4420)) & keep0,
+                                               widen(__byte_perm(b1, 0, 0x4420)) & keep1);
+                                mma16816<true>(o[2 * (j + x) + 1], a, widen(__byte_perm(b0, 0, 0x4431)) & keep0,
+                                               widen(__byte_perm(b1, 0, 0x4431)) & keep1);
+                            }
                         }
                     }
                 }
-            }
+            };
+            if (key0 + KW > g.x.key_hi || key0 < g.x.key_lo)
+                values(Bool<true>{});
+            else
+                values(Bool<false>{});
         };
 
         bool ok = true;
         for (int u = g.u_begin; ok && u < g.u_end; ++u, ++it) {
-            // Every warp waits for and releases every unit, also the ones that other slots take: a warp that skipped a stage's phase could not tell the one after next by its parity.
+            const bool mine = (slot / SPU & (turns - 1)) == (int)(it & (turns - 1));
+            if (own && !mine) continue;
             const int s = it % C::NST;
             ok = mbar_wait(&full[s], (it / C::NST) & 1, p.err, &abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t *st = ring + s * C::STAGE;
             const int key0 = (g.x.u0 + u) * UNIT;
-            if ((slot / SPU & (turns - 1)) == (int)(it & (turns - 1)))
+            if (mine)
                 for (int sl = slot % SPU; sl < SPU; sl += nslot) slice(st, key0 + sl * KW, sl);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
@@ -593,7 +611,7 @@ bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int p
                                    : dtype == DSA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     return make_tmap_4d(m, base, dt, dims, strides, box,
-                        inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                        inner * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, D * e);
 }
 
 template <int D, bool IO_F16, bool E4M3, int KW>
