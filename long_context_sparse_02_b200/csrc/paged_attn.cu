@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         p.rec[blockIdx.x].valid = 0;
     }
     pdl_trigger();
-    plan_cta<UNIT>(p, blockIdx.x, gridDim.x, plan);  // also orders the barrier setup before its use
-    Cursor cur = plan.cur;
+    Cursor cur = plan_cta<UNIT>(p, blockIdx.x, gridDim.x, plan);  // also orders the barrier setup before its use
     Segment g;
 
     if (warp >= CW) {
@@ -402,6 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         }
         // ---- join the key slots, the upper half into the lower one, in a fixed order ----
+        const bool two = rbase + 8 < last_row;  // (the group's upper eight rows are there)
         for (int half = nslot >> 1; half > 0; half >>= 1) {
             const int cell = (slot >= half ? slot - half : slot) * MT + rg;
             float *mo = merge + cell * 16 * (C::MERGE_ROW + 2);
@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * KS; ++i) {
                     *reinterpret_cast<float2 *>(mo + gid * C::MERGE_ROW + i * 8 + tig * 2) = make_float2(o[i][0], o[i][1]);
-                    *reinterpret_cast<float2 *>(mo + (gid + 8) * C::MERGE_ROW + i * 8 + tig * 2) =
-                        make_float2(o[i][2], o[i][3]);
+                    if (two)
+                        *reinterpret_cast<float2 *>(mo + (gid + 8) * C::MERGE_ROW + i * 8 + tig * 2) =
+                            make_float2(o[i][2], o[i][3]);
                 }
                 if (tig == 0)
 #pragma unroll
@@ -431,9 +432,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * KS; ++i) {
                     const float2 x = *reinterpret_cast<const float2 *>(mo + gid * C::MERGE_ROW + i * 8 + tig * 2);
-                    const float2 y = *reinterpret_cast<const float2 *>(mo + (gid + 8) * C::MERGE_ROW + i * 8 + tig * 2);
                     o[i][0] = o[i][0] * fa[0] + x.x * fb[0], o[i][1] = o[i][1] * fa[0] + x.y * fb[0];
-                    o[i][2] = o[i][2] * fa[1] + y.x * fb[1], o[i][3] = o[i][3] * fa[1] + y.y * fb[1];
+                    if (two) {
+                        const float2 y = *reinterpret_cast<const float2 *>(mo + (gid + 8) * C::MERGE_ROW + i * 8 + tig * 2);
+                        o[i][2] = o[i][2] * fa[1] + y.x * fb[1], o[i][3] = o[i][3] * fa[1] + y.y * fb[1];
+                    }
                 }
             }
             named_bar_sync(1, CW * 32);
@@ -480,7 +483,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (g.slot() == 1 && !whole && rg == 0 && lane == 0)
-                p.rec[blockIdx.x] = PieceRec{1, g.b, g.h, g.t, cur.at - (g.u_end - g.u_begin) + g.x.nu, cur.total};
+                p.rec[blockIdx.x] = PieceRec{
+                    1, g.s.q0, g.h, g.x.row0, g.x.rows, cur.at - (g.u_end - g.u_begin) + g.x.nu, cur.total};
         }
     }
 }
@@ -495,10 +499,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
     const int c = blockIdx.x, lane = lane_id();
     const PieceRec rec = p.rec[c];
     if (!rec.valid) return;
-    const SeqInfo s = seq_info(p, rec.b);
-    const int row0 = rec.t * p.TM, rows = min(p.TM, s.n * p.G - row0);
     const int r = blockIdx.y * JOIN_WARPS + warp_id();
-    if (r >= rows) return;
+    if (r >= rec.rows) return;
     const Line line(rec.total, nc);
     const int last = min(line.next(rec.end), nc);  // pieces: slot 1 of c, slot 0 of c + 1 .. last - 1
     auto at = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.TM + r; };
@@ -507,25 +509,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
     for (int base = c; base < last; base += 32) {  // 32 pieces at a time, a lane each for their weights
-        const int mine = base + lane;
-        const float ls = mine < last && (mine == c || line.start(mine) < line.start(mine + 1)) ? p.part_l[at(mine)] : -INFINITY;
-        float top = ls;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fmaxf(top, mx);
-        if (top == -INFINITY) continue;
-        const float f = ex2_approx(mx - top), w = ex2_approx(ls - top);
-        mx = top;
-        sum *= f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] *= f;
-        const int cnt = min(32, last - base);
-        for (int i0 = 0; i0 < cnt; i0 += 8) {  // eight rows in flight
-            float o[8][V];
+        const int mine = base + lane, cnt = min(32, last - base);
+        float o[8][V];
+        auto load = [&](int i0) {  // eight rows in flight, the first before their weights are known
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
-                const bool some = i0 + i < cnt && wi > 0.f;  // (a piece without weight may be unwritten)
+                const bool some = i0 + i < cnt;
                 const float *src = p.part_o + at(base + i0 + i) * D + lane * V;
                 if (V == 4) {
                     const float4 t = some ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -535,18 +524,36 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
                     o[i][0] = t.x, o[i][1] = t.y;
                 }
             }
+        };
+        load(0);
+        const float ls = mine < last && (mine == c || line.start(mine) < line.start(mine + 1)) ? p.part_l[at(mine)] : -INFINITY;
+        float top = ls;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, mx);
+        if (top == -INFINITY) continue;
+        const float f = ex2_approx(mx - top), w = ex2_approx(ls - top);
+        mx = top;
+        sum *= f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] *= f;
+        for (int i0 = 0;;) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float wi = i0 + i < cnt ? __shfl_sync(0xffffffffu, w, (i0 + i) & 31) : 0.f;
-                sum += wi;
+                const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+                if (i0 + i < cnt && wi > 0.f) {  // (a piece without weight may be unwritten)
+                    sum += wi;
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] = fmaf(wi, o[i][j], acc[j]);
+                    for (int j = 0; j < V; ++j) acc[j] = fmaf(wi, o[i][j], acc[j]);
+                }
             }
+            if ((i0 += 8) >= cnt) break;
+            load(i0);
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int row = row0 + r, tok = p.by_G.div(row);
-    const int64_t orow = (int64_t)(s.q0 + tok) * p.H + rec.h * p.G + (row - tok * p.G);
+    const int row = rec.row0 + r, tok = p.by_G.div(row);
+    const int64_t orow = (int64_t)(rec.q0 + tok) * p.H + rec.h * p.G + (row - tok * p.G);
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow * D + lane * V);
 #pragma unroll
     for (int j = 0; j < V; j += 2) dst[j / 2] = paged_pack2<IO_F16>(acc[j] * inv, acc[j + 1] * inv);

@@ -107,7 +107,7 @@ __device__ __forceinline__ Stream stream_info(const PagedAttnParams &p, const Se
 struct Walk {
     Cursor cur;
     int64_t end;
-    int b, h, t, whole, slot, row0;
+    int h, whole, slot, row0, q0, tile_row0, tile_rows;
 };
 
 // 32 scores to weights 2^(c s - mc), rounded to the values' type and packed into out[0..15]; the sum of the
@@ -288,8 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == MMA_WARP) tmem_alloc(&tmem_slot, 512);
     pdl_trigger();
     PlanShared &plan = *reinterpret_cast<PlanShared *>(ring);  // before the ring's first use
-    plan_cta<UNIT>(p, blockIdx.x, gridDim.x, plan);
-    Cursor cur = plan.cur;
+    Cursor cur = plan_cta<UNIT>(p, blockIdx.x, gridDim.x, plan);
     fence_proxy_async_smem();  // the plan's stores before the copies into the same memory
     tc_fence_before();
     __syncthreads();
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) {
                     wk.cur = cu;
                     wk.end = cu.at - (g.u_end - g.u_begin) + g.x.nu;
-                    wk.b = g.b, wk.h = g.h, wk.t = g.t;
+                    wk.h = g.h, wk.q0 = g.s.q0, wk.tile_row0 = g.x.row0, wk.tile_rows = g.x.rows;
                     wk.whole = g.whole(), wk.slot = g.slot();
                     wk.row0 = g.s.q0 - (g.s.L - g.s.n);
                 }
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (threadIdx.x == 0 && wk.slot == 1 && !whole)
-                p.rec[blockIdx.x] = PieceRec{1, wk.b, wk.h, wk.t, wk.end, wk.cur.total};
+                p.rec[blockIdx.x] = PieceRec{1, wk.q0, wk.h, wk.tile_row0, wk.tile_rows, wk.end, wk.cur.total};
             __syncwarp();  // the walk's state is read before the next segment's is written
             tc_fence_before();  // the reads of O before the next segment's first product, which waits for its weights
         }

@@ -40,8 +40,8 @@ struct PagedAttnParams {
 
 // A tile that began in this CTA and goes on in the next ones.
 struct PieceRec {
-    int32_t valid, b, h, t;
-    int64_t end, total;  // where the tile's units end on the line; the line's length
+    int32_t valid, q0, h, row0, rows;  // the sequence's first row of q; the K/V head; packed rows
+    int64_t end, total;                // where the tile's units end on the line; the line's length
 };
 
 struct SeqInfo {
@@ -127,12 +127,40 @@ struct PlanShared {
     int found;
 };
 
-// All threads of the block; the result is in sh.cur for all of them.
+// Where CTA c begins.  All threads of the block; a barrier of the block is among it.
 template <int UNIT>
-__device__ void plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh) {
+__device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh) {
     const int lane = lane_id(), warp = warp_id(), nw = blockDim.x >> 5;
     const int B = p.pg.num_seqs;
     const bool single = (int64_t)p.max_q * p.G <= p.TM;  // one tile a sequence at most
+    if (single && B <= 32) {
+        // small batches of single tokens, where the plan's latency counts: every warp by itself, a lane a sequence
+        int64_t per_head = 0;
+        if (lane < B) {
+            const SeqInfo s = seq_info(p, lane, c == 0 && warp == 0);
+            if (s.n) per_head = tile_info<UNIT>(p, s, 0).nu;
+        }
+        const int64_t w = per_head * p.Hkv;
+        int64_t inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, inc, 31);
+        const Line line(total, nc);
+        Cursor cur{0, 0, 0, 0, line.start(c), line.start(c + 1), total};
+        const uint32_t past = __ballot_sync(0xffffffffu, inc > cur.at);
+        if (cur.at < cur.end && past) {
+            cur.b = __ffs(past) - 1;
+            const int64_t off = cur.at - __shfl_sync(0xffffffffu, inc - w, cur.b);
+            const int64_t ph = __shfl_sync(0xffffffffu, per_head, cur.b);
+            cur.h = (int)div64(off, ph);
+            cur.u = (int)(off - cur.h * ph);
+        }
+        __syncthreads();
+        return cur;
+    }
     auto fill = [&](int base, bool report) {
         const int cnt = min(PLAN_SEQS, B - base);
         if (single) {
@@ -171,7 +199,7 @@ __device__ void plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh
     const int64_t begin = line.start(c), end = line.start(c + 1);
     if (threadIdx.x == 0) sh.cur = Cursor{0, 0, 0, 0, begin, end, total};
     __syncthreads();
-    if (begin >= end) return;
+    if (begin >= end) return sh.cur;
     int64_t before = 0;  // warp 0: units before the group of 32 sequences looked at
     for (int base = 0; base < B; base += PLAN_SEQS) {
         const int cnt = B > PLAN_SEQS ? fill(base, false) : B;
@@ -224,6 +252,7 @@ __device__ void plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh
         if (sh.found) break;
     }
     __syncthreads();
+    return sh.cur;
 }
 
 // A run of units of one tile that a CTA works on.
