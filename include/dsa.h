@@ -394,7 +394,7 @@ dsa_status dsa_rope_frequencies(int32_t dim, double base, int32_t scheme, double
  *   pos    device int32 [T]: any value
  * rope->offset + rope->dim <= D.  Arrays that are 16-byte aligned with strides,
  * offset and dim/2 multiples of 8 take the vectorised path; others are served
- * too.  Needs no workspace. */
+ * too.  dim up to 50000.  Needs no workspace. */
 dsa_status dsa_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t Hq, void *q_out,
                     int64_t q_out_token_stride, int64_t q_out_head_stride, const void *k, int64_t k_token_stride,
                     int64_t k_head_stride, int32_t Hk, void *k_out, int64_t k_out_token_stride,
@@ -460,7 +460,8 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  * Softmax statistics and sums are fp32; the softmax weights enter the second
  * product in the q type (fp16 for an E4M3 cache).  Results do not depend on
  * what else is in the call's timing: no atomics, a fixed order of sums.
- * Supported: Dk == Dv in {64, 128}, H a multiple of heads. */
+ * Supported: Dk == Dv in {64, 128}, H a multiple of heads; T, max_q, max_len up to
+ * 2^30, T * H below 2^31. */
 size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, const dsa_kv_cache *cache,
                                       int32_t max_q, int32_t max_len, int32_t window);
 dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t H,

@@ -596,6 +596,7 @@ size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, co
     if (T <= 0 || num_seqs <= 0 || H <= 0 || !cache || cache->heads <= 0 || H % cache->heads || max_q <= 0 ||
         max_len <= 0 || window < 0)
         return 0;
+    if (window >= max_len) window = 0;  // as dsa_paged_attn takes it
     const DeviceInfo *dev = current_device();
     return paged_attn_workspace_bytes(T, num_seqs, H, cache->heads, cache->Dk, cache->dtype, max_q, max_len, window,
                                       dev ? dev->sm_count : 148);
@@ -614,7 +615,10 @@ dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_
     if (!cache->v || cache->Dk != cache->Dv || (cache->Dk != 64 && cache->Dk != 128) || H % cache->heads)
         return DSA_ERR_UNSUPPORTED;
     if (T == 0) return DSA_OK;
-    if ((int64_t)T * H >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    // positions, and their differences to a window's, stay within 32 bits
+    constexpr int32_t most = 1 << 30;
+    if (T > most || max_q > most || max_len > most || (int64_t)T * H >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    if (window >= max_len) window = 0;  // all of it is within the window
     if (!q || !out || !aligned16(q) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     if ((T > 1 && (q_token_stride & 7)) || (H > 1 && (q_head_stride & 7))) return DSA_ERR_INVALID_ARG;
     PagedAttnArgs a{{q, q_token_stride, H > 1 ? q_head_stride : 0, H}, cache, paged_dev(pg), q_start, T, max_q,

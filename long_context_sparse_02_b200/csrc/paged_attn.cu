@@ -598,11 +598,11 @@ Plan make_plan(int TM, int unit, int num_seqs, int G, int Hkv, int D, int max_q,
 bool tc_shape(int G, int max_q, int cache_dtype) {
     return cache_dtype != DSA_E4M3 && G <= 128 && (int64_t)max_q * G > 64;
 }
-// What else the tensor-core kernel needs of a call: a positive scale (the
-// maximum is taken before scaling) and q reachable by a tensor map.
+// What else the tensor-core kernel needs of a call: a positive scale that stays
+// one in fp32 (the maximum is taken before scaling) and q reachable by a tensor map.
 bool tc_call(const PagedAttnArgs &a) {
     auto ok = [](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < ((int64_t)1 << 39)); };
-    return a.sm_scale > 0 && ok(a.q.token_stride, a.T) && ok(a.q.head_stride, a.q.heads);
+    return a.sm_scale > 1e-30f && ok(a.q.token_stride, a.T) && ok(a.q.head_stride, a.q.heads);
 }
 
 bool kv_map(CUtensorMap *m, const void *base, int dtype, int D, int heads, int pages, int64_t page, int64_t row,

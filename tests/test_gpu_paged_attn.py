@@ -87,7 +87,7 @@ def test_attention(L, lens, new, H, Hkv, D, dtype, cdt):  # noqa: F811
     c.check(*c.run())
 
 
-@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 129, 1000, 1 << 30])
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 129, 1000, 2 ** 31 - 1])
 @pytest.mark.parametrize("lens,new,H,Hkv,D,cdt", [([700, 64, 1], [1, 1, 1], 8, 2, 128, None),
                                                   ([700, 64, 90], [300, 64, 3], 6, 2, 128, None),
                                                   ([515, 140], [200, 1], 4, 4, 64, E4M3)])
@@ -130,6 +130,25 @@ def test_empty_and_untouched(L, D):  # noqa: F811
     c.run(out=out, lse=lse)
     no_error(L)
     assert (out == 5.0).all()
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_one_query_for_all_and_an_odd_output(L, new):  # noqa: F811
+    """A query given to every token by a stride of 0, and outputs that begin 16 bytes off a 32-byte boundary."""
+    c = Case(L, [300, 90], [new, new], 4, 2, 128)
+    one = c.q[:1].expand(c.T, 4, 128)
+    c.q = one.contiguous()
+    want, lse = c.run()
+    c.check(want, lse)
+    got, _ = c.run(q=one)
+    for b in range(2):
+        rows = slice(b * new, (b + 1) * new)
+        ref.assert_attended(got[rows], c.ref(b))
+    room = torch.zeros(want.numel() + 8, device="cuda", dtype=BF16)
+    odd = room[8:].view(want.shape)
+    c.run(out=odd)
+    no_error(L)
+    assert torch.equal(odd, want) and (room[:8] == 0).all()
 
 
 def test_decode_without_q_start(L):  # noqa: F811
@@ -177,8 +196,9 @@ def test_bounds_are_checked_on_the_device(L):  # noqa: F811
     c.check(*c.run())
 
 
-def test_bad_pages_read_as_zeros(L):  # noqa: F811
-    c = Case(L, [200], [1], 2, 1, 64)
+@pytest.mark.parametrize("new,cdt", [(1, None), (1, E4M3), (150, None)])
+def test_bad_pages_read_as_zeros(L, new, cdt):  # noqa: F811
+    c = Case(L, [200], [new], 2, 1, 64, BF16, cdt)
     c.table[0, 1] = c.pages
     out, lse = c.run()
     no_error(L, L.DEVERR_PAGE)

@@ -199,6 +199,40 @@ def test_append(L, lens, new, H, Hkv, Dk, Dv, dim, offset, inter, dtype, cdt, or
         assert torch.equal(bits(c), was)
 
 
+@pytest.mark.parametrize("cdt", [BF16, torch.uint8])
+def test_append_from_odd_places(L, cdt):
+    """New rows as slices that begin off 16-byte boundaries, many heads of one token, and a cache of one page."""
+    g = gen(12)
+    kc = torch.zeros(1, 64, 40, 64, device="cuda", dtype=cdt)
+    vc = torch.zeros_like(kc)
+    seq_lens = torch.tensor([64], device="cuda", dtype=torch.int32)
+    pg = L.paged(seq_lens, torch.zeros(1, 1, device="cuda", dtype=torch.int32), 1)
+    cache = L.kv_cache(kc, vc, 16.0, 16.0)
+    freq = L.rope_frequencies(32)[0].cuda()
+    spec = L.rope_spec(freq, 16, False)
+    fused = randn(g, 3, 120 * 64 + 1)[:, 1:].unflatten(1, (120, 64))
+    k, v, q = fused[:, :40], fused[:, 40:80], fused[:, 80:]
+    pos = torch.tensor([63, 0, 31], device="cuda", dtype=torch.int32)
+    seq = torch.zeros(3, device="cuda", dtype=torch.int32)
+    qo = L.append_rope(k, v, seq, pos, pg, cache, spec, q=q)
+    no_error(L)
+    ref.assert_rotated(qo, ref.rotate(q, pos, freq, 16), q)
+    want = ref.rotate(k, pos, freq, 16)
+    if cdt == BF16:
+        ref.assert_rotated(kc[0, pos.long()], want, k)
+        assert torch.equal(vc[0, pos.long()], v)
+    else:
+        for c, x in ((kc, want), (vc, v.double())):
+            got = c[0, pos.long()].view(torch.float8_e4m3fn).double()
+            assert ((got - 16 * x).abs() <= 2.0 ** -4 * (16 * x).abs() + 2.0 ** -10 + 2.0 ** -17 * 64).all()
+    # q rotated in place: the elements around the rotated part stay
+    mine = q.clone()
+    kc.zero_(), vc.zero_()
+    assert L.append_rope(k, v, seq, pos, pg, cache, spec, q=mine, q_out=mine) is mine
+    no_error(L)
+    assert torch.equal(mine, qo)
+
+
 def test_append_skips(L):
     """Padding, sequences and positions out of range, bad pages: those tokens write nothing, the others as ever."""
     g = gen(9)

@@ -126,6 +126,8 @@ def test_attention_refused(L):
     for kw in (dict(H=7), dict(cache=cache(L, v=None, Dv=0)), dict(cache=cache(L, Dv=64)), dict(cache=cache(L, Dk=96, Dv=96)),
                dict(cache=cache(L, Dk=576, Dv=576))):
         assert call_attn(L, **kw) == 2, kw
+    for kw in (dict(max_len=(1 << 30) + 1), dict(max_q=(1 << 30) + 1), dict(T=(1 << 30) + 1), dict(T=1 << 30)):
+        assert call_attn(L, **kw) == 2, kw
     assert call_attn(L, T=0) == 0
 
 
@@ -136,6 +138,7 @@ def test_workspace_size(L):
                 (8, 8, 64, cache(L), 0, 1000, 0), (8, 8, 64, cache(L), 1, 0, 0), (8, 8, 64, cache(L), 1, 1000, -1),
                 (8, 8, 64, None, 1, 1000, 0)):
         assert f(*bad) == 0
+    assert f(8, 8, 64, cache(L), 1, 1000, 1000) == f(8, 8, 64, cache(L), 1, 1000, 0) == f(8, 8, 64, cache(L), 1, 1000, 2 ** 31 - 1)
     # a bound, whatever the lengths: no more for a million positions than for a few thousand
     assert f(8, 8, 64, cache(L), 1, 1 << 20, 0) == f(8, 8, 64, cache(L), 1, 1 << 16, 0)
 
