@@ -598,7 +598,7 @@ size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, co
         return 0;
     if (window >= max_len) window = 0;  // as dsa_paged_attn takes it
     const DeviceInfo *dev = current_device();
-    return paged_attn_workspace_bytes(T, num_seqs, H, cache->heads, cache->Dk, cache->dtype, max_q, max_len, window,
+    return paged_attn_workspace_bytes(num_seqs, H, cache->heads, cache->Dk, cache->dtype == DSA_E4M3, max_q, max_len, window,
                                       dev ? dev->sm_count : 148);
 }
 

@@ -214,8 +214,8 @@ struct PagedAttnArgs {
     void *ws;
     size_t ws_bytes;
 };
-size_t paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, int32_t cache_dtype,
-                                  int32_t max_q, int32_t max_len, int32_t window, int sm_count);
+size_t paged_attn_workspace_bytes(int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, bool e4m3, int32_t max_q,
+                                  int32_t max_len, int32_t window, int sm_count);
 dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st);
 
 // ---- context-parallel decode: joining the ranks' partial results -----------------

@@ -95,13 +95,6 @@ struct Bool {
     static constexpr bool value = B;
 };
 
-// Two e4m3 codes (bits 0-15) to fp16 (exact).
-__device__ __forceinline__ uint32_t widen(uint32_t v) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(v));
-    return r;
-}
-
 // MT = TM / 16 row groups of 16; the consumer warps are MT row groups x CW/MT
 // key slots.  A unit has 64 / KW slices of KW keys; where a row group has more
 // slots than that, they take turns unit by unit.
@@ -280,10 +273,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < NT; i += 2) {
                         uint32_t b[4];
                         ldsm4(b, kb + tile_off<C::BOX_BYTES>(row + i * 8, k + ch));
-                        mma16816<true>(s[i], qf[k], widen(b[0]), widen(b[0] >> 16));
-                        mma16816<true>(s[i + 1], qf[k], widen(b[1]), widen(b[1] >> 16));
-                        mma16816<true>(s[i], qf[k + 1], widen(b[2]), widen(b[2] >> 16));
-                        mma16816<true>(s[i + 1], qf[k + 1], widen(b[3]), widen(b[3] >> 16));
+                        mma16816<true>(s[i], qf[k], paged_widen(b[0]), paged_widen(b[0] >> 16));
+                        mma16816<true>(s[i + 1], qf[k], paged_widen(b[1]), paged_widen(b[1] >> 16));
+                        mma16816<true>(s[i], qf[k + 1], paged_widen(b[2]), paged_widen(b[2] >> 16));
+                        mma16816<true>(s[i + 1], qf[k + 1], paged_widen(b[3]), paged_widen(b[3] >> 16));
                     }
             }
             // scores in log2 units; masked where a row does not see the key
@@ -363,10 +356,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const uint32_t b0 = b[2 * x], b1 = b[2 * x + 1];
-                                mma16816<true>(o[2 * (j + x)], a, widen(__byte_perm(b0, 0, 0x4420)) & keep0,
-                                               widen(__byte_perm(b1, 0, 0x4420)) & keep1);
-                                mma16816<true>(o[2 * (j + x) + 1], a, widen(__byte_perm(b0, 0, 0x4431)) & keep0,
-                                               widen(__byte_perm(b1, 0, 0x4431)) & keep1);
+                                mma16816<true>(o[2 * (j + x)], a, paged_widen(__byte_perm(b0, 0, 0x4420)) & keep0,
+                                               paged_widen(__byte_perm(b1, 0, 0x4420)) & keep1);
+                                mma16816<true>(o[2 * (j + x) + 1], a, paged_widen(__byte_perm(b0, 0, 0x4431)) & keep0,
+                                               paged_widen(__byte_perm(b1, 0, 0x4431)) & keep1);
                             }
                         }
                     }
@@ -592,12 +585,12 @@ Plan make_plan(int TM, int unit, int num_seqs, int G, int Hkv, int D, int max_q,
     return pl;
 }
 
-// Chunks go to the tensor-core kernel: more packed rows a K/V head than the
-// warp-level kernel's widest tile but one, so that at least a quarter of the
-// 256-row tile is real.
-bool tc_shape(int G, int max_q, int cache_dtype) {
-    return cache_dtype != DSA_E4M3 && G <= 128 && (int64_t)max_q * G > 64;
-}
+// Few packed rows a K/V head go to the warp-level kernel, more to the tensor
+// cores.  8 sequences of 32768 positions, 8 K/V heads of 128, us (warp-level /
+// tensor cores): 2-byte cache 32 rows 171 / 204, 64 rows 264 / 208, 128 rows
+// 464 / 212; E4M3 32 rows 171 / 264, 64 rows 309 / 266 (8 x 1024: 25 / 31),
+// 96 rows 543 / 268.
+bool tc_shape(int G, int max_q, bool e4m3) { return G <= 128 && (int64_t)max_q * G > (e4m3 ? 64 : 32); }
 // What else the tensor-core kernel needs of a call: a positive scale that stays
 // one in fp32 (the maximum is taken before scaling) and q reachable by a tensor map.
 bool tc_call(const PagedAttnArgs &a) {
@@ -666,12 +659,12 @@ bool paged_kv_maps(const dsa_kv_cache &c, int num_pages, CUtensorMap *km, CUtens
            kv_map(vm, c.v, c.dtype, c.Dk, c.heads, num_pages, c.v_page_stride, c.v_row_stride, c.v_head_stride);
 }
 
-size_t paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, int32_t cache_dtype,
-                                  int32_t max_q, int32_t max_len, int32_t window, int sm_count) {
+size_t paged_attn_workspace_bytes(int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, bool e4m3, int32_t max_q,
+                                  int32_t max_len, int32_t window, int sm_count) {
     const int G = H / Hkv;
     size_t need = make_plan(16 * tile_groups((int64_t)max_q * G), UNIT, num_seqs, G, Hkv, D, max_q, max_len, window,
                             sm_count).total;
-    if (tc_shape(G, max_q, cache_dtype)) {  // (the call's scale and strides decide between the two)
+    if (tc_shape(G, max_q, e4m3)) {  // (the call's scale and strides decide between the two)
         const size_t tc =
             make_plan(paged_attn_tc_rows(G), 128, num_seqs, G, Hkv, D, max_q, max_len, window, sm_count).total;
         need = tc > need ? tc : need;
@@ -684,7 +677,7 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     if (!dev) return DSA_ERR_CUDA;
     const dsa_kv_cache &c = *a.cache;
     const int H = a.q.heads, D = c.Dk, G = H / c.heads;
-    const bool tc = tc_shape(G, a.max_q, c.dtype) && tc_call(a);
+    const bool tc = tc_shape(G, a.max_q, c.dtype == DSA_E4M3) && tc_call(a);
     const Plan pl = make_plan(tc ? paged_attn_tc_rows(G) : 16 * tile_groups((int64_t)a.max_q * G), tc ? 128 : UNIT,
                               a.pg.num_seqs, G, c.heads, D, a.max_q, a.max_len, a.window, dev->sm_count);
     if (!a.ws || a.ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(a.ws) & 255u)) return DSA_ERR_WORKSPACE;

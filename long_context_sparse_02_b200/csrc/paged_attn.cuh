@@ -18,6 +18,13 @@ __device__ __forceinline__ uint32_t paged_pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Two e4m3 codes (bits 0-15) to fp16 (exact).
+__device__ __forceinline__ uint32_t paged_widen(uint32_t v) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
                                             int32_t z) {
     asm volatile(

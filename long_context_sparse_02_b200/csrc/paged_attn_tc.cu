@@ -29,20 +29,25 @@ namespace dsa {
 namespace {
 
 constexpr int UNIT = 128;
-constexpr int THREADS = 384;  // two softmax warpgroups, one of single-warp roles
 constexpr int MMA_WARP = 8, LOAD_WARP = 10, CLEAR_WARP = 11;  // MMA_WARP + stream
-// registers: 384 x 168 at launch; the roles' shares add up to the same
-constexpr int REG_LAUNCH = 168, REG_SOFTMAX = 208, REG_REST = 88;
-static_assert(256 * REG_SOFTMAX + 128 * REG_REST == THREADS * REG_LAUNCH, "register shares");
+constexpr int WIDEN_WARP = 12;  // 8-bit caches: a warpgroup of them
 
-template <int D>
+// E4M3: keys and values arrive as 8-bit codes in a ring of their own and are widened to fp16 (exactly) into the
+// ring that the products read.
+template <int D, bool E4M3>
 struct Cfg {
     static constexpr int NH = D / 64;                 // 128-byte column blocks of a row
     static constexpr int BLOCK = 128 * 128;           // [128 rows][64 elements]
     static constexpr int TILE = NH * BLOCK;           // Q of a stream, K or V of a unit
-    static constexpr int NST = 160 * 1024 / TILE;     // ring slots (K and V alternate)
-    static constexpr int SMEM = 2 * TILE + NST * TILE + 1024;
+    static constexpr int RAW = TILE / 2;              // the same in 8 bits
+    static constexpr int NST = (E4M3 ? 96 : 160) * 1024 / TILE;  // ring slots (K and V alternate)
+    static constexpr int NRAW = E4M3 ? 48 * 1024 / RAW : 0;
+    static constexpr int SMEM = 2 * TILE + NST * TILE + NRAW * RAW + 1024;
     static constexpr uint32_t O_COL = 256;            // S0 at 0, S1 at 128, O0, O1
+    static constexpr int THREADS = E4M3 ? 512 : 384;  // two softmax warpgroups, the single-warp roles, the wideners
+    // registers: the roles' shares add up to what the block is launched with
+    static constexpr int REG_LAUNCH = E4M3 ? 128 : 168, REG_SOFTMAX = E4M3 ? 184 : 208, REG_REST = E4M3 ? 72 : 88;
+    static_assert(256 * REG_SOFTMAX + (THREADS - 256) * REG_REST == THREADS * REG_LAUNCH, "register shares");
 };
 
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
@@ -259,24 +264,32 @@ __device__ __forceinline__ bool needs_clear(const Segment &g, int key0) {
     return key0 + UNIT > g.x.key_hi || key0 < g.x.key_lo;
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(THREADS, 1)
+// IO_F16: q and out are fp16 (else bf16); the products run in fp16 when IO_F16 or the cache is E4M3.
+template <int D, bool IO_F16, bool E4M3>
+__global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const PagedAttnParams p) {
-    using C = Cfg<D>;
-    constexpr int NST = C::NST;
+    using C = Cfg<D, E4M3>;
+    constexpr int NST = C::NST, NRAW = E4M3 ? C::NRAW : 1;
+    constexpr bool F16 = IO_F16 || E4M3;         // type of the products
+    constexpr bool FIT = E4M3 && !IO_F16;        // rows of q are fitted into fp16
     extern __shared__ uint8_t smem_raw[];
     uint8_t *Qs = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *ring = Qs + 2 * C::TILE;
+    uint8_t *ring = Qs + 2 * C::TILE, *raw = ring + NST * C::TILE;
     __shared__ uint64_t full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], v_clear[NST], drain;
     __shared__ uint32_t tmem_slot;
+    __shared__ uint64_t raw_full[NRAW], raw_empty[NRAW], q_fit[2];
+    __shared__ float row_scale[FIT ? 2 : 1][2][FIT ? 128 : 1];  // by segment in turn, stream, row: what fitting took out
     __shared__ Walk walk[8];
     __shared__ int abort_flag;
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NST; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 3), mbar_init(&v_clear[s], 1);
+        // (an E4M3 cache: filled by the four widening warps, which clear values too)
+        for (int s = 0; s < NST; ++s)
+            mbar_init(&full[s], E4M3 ? 4 : 1), mbar_init(&empty[s], E4M3 ? 2 : 3), mbar_init(&v_clear[s], 1);
+        for (int s = 0; s < NRAW; ++s) mbar_init(&raw_full[s], 1), mbar_init(&raw_empty[s], 4);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
+            mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1), mbar_init(&q_fit[s], 4);
             mbar_init(&s_full[s], 1), mbar_init(&p_full[s], 4), mbar_init(&o_full[s], 1);
         }
         mbar_init(&drain, 2);
@@ -297,26 +310,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     Segment g;
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_REST));
         if (warp == LOAD_WARP) {
             // ---- producer ----
             uint32_t it = 0, qn[2] = {0, 0};  // ring slots used, loads of each stream's Q
             bool ok = true;
-            auto slot_wait = [&](uint32_t i) {
-                if (ok && i >= NST) ok = mbar_wait(&empty[i % NST], ((i / NST) - 1) & 1, p.err, &abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-            };
+            constexpr int N = E4M3 ? NRAW : NST;
+            uint64_t *const filled = E4M3 ? raw_full : full, *const freed = E4M3 ? raw_empty : empty;
             auto load_tile = [&](const CUtensorMap *map, int h, int pg0, int pg1) {  // one K or V tile
-                slot_wait(it);
+                const uint32_t slot = it % N;
+                if (ok && it >= N) ok = mbar_wait(&freed[slot], ((it / N) - 1) & 1, p.err, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 if (lane == 0) {
-                    uint64_t *bar = &full[it % NST];
-                    uint8_t *dst = ring + (it % NST) * C::TILE;
-                    mbar_expect_tx(bar, C::TILE);
+                    uint64_t *bar = &filled[slot];
+                    if (E4M3) {
+                        uint8_t *dst = raw + slot * C::RAW;
+                        mbar_expect_tx(bar, C::RAW);
+                        tma_load_4d(dst, map, bar, 0, 0, h, pg0);
+                        tma_load_4d(dst + C::RAW / 2, map, bar, 0, 0, h, pg1);
+                    } else {
+                        uint8_t *dst = ring + slot * C::TILE;
+                        mbar_expect_tx(bar, C::TILE);
 #pragma unroll
-                    for (int x = 0; x < C::NH; ++x) {
-                        tma_load_4d(dst + x * C::BLOCK, map, bar, x * 64, 0, h, pg0);
-                        tma_load_4d(dst + x * C::BLOCK + C::BLOCK / 2, map, bar, x * 64, 0, h, pg1);
+                        for (int x = 0; x < C::NH; ++x) {
+                            tma_load_4d(dst + x * C::BLOCK, map, bar, x * 64, 0, h, pg0);
+                            tma_load_4d(dst + x * C::BLOCK + C::BLOCK / 2, map, bar, x * 64, 0, h, pg1);
+                        }
                     }
                 }
                 __syncwarp();
@@ -366,8 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // an abandoned run: copies in flight end before the block's shared memory does
             if (!ok) {
-                for (uint32_t j = it > NST ? it - NST : 0; j < it; ++j)
-                    mbar_wait(&full[j % NST], (j / NST) & 1, p.err, nullptr);
+                for (uint32_t j = it > N ? it - N : 0; j < it; ++j) mbar_wait(&filled[j % N], (j / N) & 1, p.err, nullptr);
                 for (int st = 0; st < 2; ++st)
                     if (qn[st]) mbar_wait(&q_full[st], (qn[st] - 1) & 1, p.err, nullptr);
             }
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (has_pv) {
                             if (!wait(&full[vslot], vpar)) break;
                             const int key0 = key_u0 + (i - 1) * UNIT;
-                            if (needs_clear(g, key0)) {
+                            if (!E4M3 && needs_clear(g, key0)) {
                                 // (a barrier a slot: the clearing warp may be two cleared units ahead)
                                 if (!wait(&v_clear[vslot], (cpar >> vslot) & 1)) break;
                                 cpar ^= 1u << vslot;
@@ -423,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (has_s && i >= s.lo && i < s.hi) {
                             const uint64_t kd = dk + kslot * (C::TILE >> 4);
                             if (i == s.lo) {
-                                if (!wait(&q_full[st], qpar)) break;
+                                if (!wait(FIT ? &q_fit[st] : &q_full[st], qpar)) break;
                                 qpar ^= 1;
                             }
 #pragma unroll
@@ -447,7 +466,87 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_wait(&drain, 0, p.err, nullptr);
             }
             __syncwarp();
-        } else if (warp == CLEAR_WARP) {
+        } else if (E4M3 && warp >= WIDEN_WARP) {
+            // ---- 8-bit tiles to fp16, and rows of q fitted into it ----
+            const int x = threadIdx.x - WIDEN_WARP * 32;  // 0 .. 127
+            uint32_t it = 0, qn[2] = {0, 0};              // tiles; loads of each stream's Q
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && mbar_wait(bar, parity, p.err, &abort_flag);
+                return ok = __all_sync(0xffffffffu, ok);
+            };
+            auto widen_tile = [&](int key0, bool clear) {
+                const uint32_t from = it % NRAW, to = it % NST;
+                if (!wait(&raw_full[from], (it / NRAW) & 1)) return;
+                if (it >= NST && !wait(&empty[to], ((it / NST) - 1) & 1)) return;
+                const uint8_t *src = raw + from * C::RAW;
+                uint8_t *dst = ring + to * C::TILE;
+                constexpr int CH = D / 16;  // 16-byte chunks of a row's codes
+#pragma unroll 4
+                for (int i = x; i < 128 * CH; i += 128) {
+                    const int row = i / CH, ch = i % CH;
+                    const uint32_t at = CH == 8 ? row * 128 + ((ch ^ (row & 7)) << 4) : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+                    uint4 v = *reinterpret_cast<const uint4 *>(src + at);
+                    // (values at positions that no row of the tile sees may be anything: zeros instead)
+                    if (clear && (key0 + row < g.x.key_lo || key0 + row >= g.x.key_hi)) v = make_uint4(0, 0, 0, 0);
+                    uint8_t *out = dst + (ch >> 2) * C::BLOCK + row * 128;
+                    const int c0 = (ch & 3) * 2, sw = row & 7;
+                    *reinterpret_cast<uint4 *>(out + ((c0 ^ sw) << 4)) =
+                        make_uint4(paged_widen(v.x), paged_widen(v.x >> 16), paged_widen(v.y), paged_widen(v.y >> 16));
+                    *reinterpret_cast<uint4 *>(out + (((c0 + 1) ^ sw) << 4)) =
+                        make_uint4(paged_widen(v.z), paged_widen(v.z >> 16), paged_widen(v.w), paged_widen(v.w >> 16));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&raw_empty[from]), mbar_arrive(&full[to]);
+                ++it;
+            };
+            while (ok && next_segment<UNIT>(p, cur, g)) {
+                if (FIT) {
+                    for (int st = 0; ok && st < 2; ++st) {
+                        const Stream s = stream_info(p, g, st);
+                        if (s.lo >= s.hi) continue;
+                        if (!wait(&q_full[st], qn[st] & 1)) break;
+                        // this thread's row times 2^-e, 2^e <= max |q| < 2^(e+1): what fp16 loses lies 2^-24 below
+                        // the row's largest element (rows past the stream's hold nothing of use)
+                        uint8_t *row = Qs + st * C::TILE + x * 128;
+                        float mx = 0.f;
+#pragma unroll 2
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(row + (i >> 3) * C::BLOCK + (i & 7) * 16);
+                            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(q[j] << 16)), fabsf(__uint_as_float(q[j] & 0xFFFF0000u))));
+                        }
+                        int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                        e = mx > 0.f ? max(-126, min(e, 126)) : 0;
+                        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 2
+                        for (int i = 0; i < D / 8; ++i) {
+                            uint4 *at = reinterpret_cast<uint4 *>(row + (i >> 3) * C::BLOCK + (i & 7) * 16);
+                            const uint4 v = *at;
+                            uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                q[j] = paged_pack2<true>(__uint_as_float(q[j] << 16) * down,
+                                                         __uint_as_float(q[j] & 0xFFFF0000u) * down);
+                            *at = make_uint4(q[0], q[1], q[2], q[3]);
+                        }
+                        row_scale[FIT ? qn[st] & 1 : 0][st][FIT ? x : 0] = __uint_as_float((uint32_t)(127 + e) << 23);
+                        ++qn[st];
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&q_fit[st]);
+                    }
+                }
+                for (int i = g.u_begin; ok && i < g.u_end; ++i) {
+                    const int key0 = (g.x.u0 + i) * UNIT;
+                    widen_tile(key0, false);
+                    if (ok) widen_tile(key0, needs_clear(g, key0));
+                }
+            }
+        } else if (!E4M3 && warp == CLEAR_WARP) {
             // ---- values at positions that no row of the tile sees may be anything (unwritten rows, other
             // sequences'): weights of 0 do not silence a NaN, so they are set to zero before their product ----
             int slot = 0;
@@ -485,12 +584,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFTMAX));
         // ---- softmax and output of stream st: thread r holds row r ----
         const int st = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter: lane 32 x (warp % 4), bits 16 up
         const uint32_t ts = tmem + lanes + st * 128, to = tmem + lanes + C::O_COL + st * 128;
-        const float c = p.scale_log2;
+        float c = p.scale_log2;
         uint32_t sn = 0, on = 0;  // S tiles and outputs waited for
         bool ok = true;
         // A row of scores needs 128 registers: the walk's state waits in shared memory meanwhile.
@@ -528,6 +627,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 ++sn;
                 tc_fence_after();
+                // (the products that these scores come from waited for the row's fitting; `on` segments had any before)
+                if (FIT && first) c = p.scale_log2 * row_scale[on & 1][st][FIT ? r : 0];
                 if (key0 + UNIT - 1 <= p_min && (!p.window || key0 > p_max - p.window))
                     softmax_tile<D, F16>(ts, to, c, first, m, l);
                 else
@@ -544,7 +645,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
             }
             const bool whole = wk.whole;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l > 0.f ? p.v_inv / l : 0.f;
             const float ls = l > 0.f ? m * c + log2f(l) : -INFINITY;
             const int64_t orow = (int64_t)(wk.row0 + p_first + tok) * p.H + wk.h * p.G + (r - tok * p.G);
             const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + st * (p.TM / 2) + r;
@@ -569,7 +670,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (whole) {
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
-                        o[q] = paged_pack2<F16>(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1]));
+                        o[q] = paged_pack2<IO_F16>(__uint_as_float(o[2 * q]), __uint_as_float(o[2 * q + 1]));
                     store32(orow_p + j, o, wide), store32(orow_p + j + 16, o + 8, wide);
                 } else {
                     float *dst = p.part_o + piece * D + j;
@@ -591,25 +692,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-template <int D, bool F16>
+template <int D, bool IO_F16, bool E4M3>
 dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
-    auto fn = paged_attn_tc_kernel<D, F16>;
+    using C = Cfg<D, E4M3>;
+    auto fn = paged_attn_tc_kernel<D, IO_F16, E4M3>;
     // the roles' register shares draw on what the block was launched with
     static const bool regs_ok = [fn] {
         cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, fn) == cudaSuccess && fa.numRegs == REG_LAUNCH;
+        return cudaFuncGetAttributes(&fa, fn) == cudaSuccess && fa.numRegs == C::REG_LAUNCH;
     }();
-    if (!regs_ok || !ensure_smem(reinterpret_cast<const void *>(fn), Cfg<D>::SMEM)) return DSA_ERR_CUDA;
+    if (!regs_ok || !ensure_smem(reinterpret_cast<const void *>(fn), C::SMEM)) return DSA_ERR_CUDA;
     CUtensorMap qm, km, vm;
     if (!paged_kv_maps(*a.cache, a.pg.num_pages, &km, &vm)) return DSA_ERR_CUDA;
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.H, (uint64_t)p.T};
     const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)(p.TM / 2 / p.G)};
     const uint64_t hs = (uint64_t)(p.H > 1 ? p.q_head : D) * 2, ts = (uint64_t)(p.T > 1 ? p.q_token : D) * 2;
-    if (!make_tmap_3d(&qm, p.q, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, hs, ts, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!make_tmap_3d(&qm, p.q, IO_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, hs, ts,
+                      box, CU_TENSOR_MAP_SWIZZLE_128B))
         return DSA_ERR_CUDA;
-    fn<<<nc, THREADS, Cfg<D>::SMEM, st>>>(qm, km, vm, p);
+    fn<<<nc, C::THREADS, C::SMEM, st>>>(qm, km, vm, p);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+template <int D>
+dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    const bool f16 = a.dtype == DSA_F16;
+    if (a.cache->dtype == DSA_E4M3) return f16 ? launch<D, true, true>(a, p, nc, st) : launch<D, false, true>(a, p, nc, st);
+    return f16 ? launch<D, true, false>(a, p, nc, st) : launch<D, false, false>(a, p, nc, st);
 }
 
 }  // namespace
@@ -617,9 +726,7 @@ dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cuda
 int paged_attn_tc_rows(int G) { return 2 * (128 / G) * G; }
 
 dsa_status launch_paged_attn_tc(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
-    const bool f16 = a.dtype == DSA_F16;
-    if (a.cache->Dk == 128) return f16 ? launch<128, true>(a, p, nc, st) : launch<128, false>(a, p, nc, st);
-    return f16 ? launch<64, true>(a, p, nc, st) : launch<64, false>(a, p, nc, st);
+    return a.cache->Dk == 128 ? launch<128>(a, p, nc, st) : launch<64>(a, p, nc, st);
 }
 
 }  // namespace dsa

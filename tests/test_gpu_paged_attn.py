@@ -272,17 +272,19 @@ def test_long_streams(L, D, cdt, new):  # noqa: F811
         ref.assert_attended(out[rows], c.ref(b), lse[rows], F16 if cdt == E4M3 else None)
 
 
-@pytest.mark.parametrize("Hkv,window", [(16, 128), (16, 100), (4, 300), (2, 0)])
-def test_long_chunks(L, Hkv, window):  # noqa: F811
+@pytest.mark.parametrize("Hkv,window,dtype,cdt", [(16, 128, BF16, None), (16, 100, F16, None), (4, 300, BF16, None),
+                                                  (2, 0, BF16, None), (16, 128, BF16, E4M3), (2, 0, F16, E4M3),
+                                                  (4, 500, BF16, E4M3)])
+def test_long_chunks(L, Hkv, window, dtype, cdt):  # noqa: F811
     """Many short segments a CTA, each with keys to leave out at both ends."""
     lens, new = [2048, 3000, 2500, 1300, 4000, 700], [1999, 2000, 1024, 1300, 257, 129]
-    c = Case(L, lens, new, 16, Hkv, 128)
+    c = Case(L, lens, new, 16, Hkv, 128, dtype, cdt)
     out, lse = c.run(window)
     no_error(L)
     for b in range(6):
         at = int(c.q_start[b])
         rows = torch.cat((torch.arange(0, 60), torch.arange(new[b] // 2, new[b] // 2 + 60), torch.arange(new[b] - 9, new[b]))).cuda()
-        ref.assert_attended(out[at + rows], c.ref(b, window, rows=rows), lse[at + rows])
+        ref.assert_attended(out[at + rows], c.ref(b, window, rows=rows), lse[at + rows], F16 if cdt else None)
 
 
 def test_long_offsets(L):  # noqa: F811
