@@ -15,6 +15,11 @@
 // and values go from swizzled shared memory to the fragments by ldmatrix; an
 // 8-bit cache is widened to fp16 (exact) in registers, one conversion for two
 // values, and the rows of q are scaled by a power of two to fit fp16 exactly.
+//
+// Measured: 64 sequences of 4096-65536 positions, one token each, 64 heads of
+// 128 on 8, bf16: 1256-1330 us for 8.95 GB (the measured copy rate); 33
+// sequences over an E4M3 cache 285-309 us for 1.43 GB (71-77% of it: twice the
+// instructions a byte); one token over 4097 positions 15 us on the device.
 #include <cuda_fp16.h>
 
 #include "dsa_device.cuh"
