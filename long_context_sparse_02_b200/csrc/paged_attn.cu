@@ -24,77 +24,26 @@
 
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
-#include "paged_attn.cuh"
+#include "paged_units.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int UNIT = 64;
+constexpr int UNIT = UNIT_KEYS;
 constexpr int CW = 8;  // consumer warps
 constexpr int THREADS = (CW + 4) * 32;  // and a warpgroup of which one warp loads
 // registers: 384 x 168 at launch; the roles' shares add up to the same
 constexpr int REG_LAUNCH = 168, REG_CONSUME = 216, REG_LOAD = 72;
 static_assert(CW * 32 * REG_CONSUME + 128 * REG_LOAD == THREADS * REG_LAUNCH, "register shares");
-constexpr int RING_BYTES = 160 * 1024;
 constexpr int MERGE_LD = 4;  // floats of padding per merged row
 
 template <int D, bool E4M3>
-struct Cfg {
-    static constexpr int ELEM = E4M3 ? 1 : 2;
-    static constexpr int ROW_BYTES = D * ELEM;                            // of one head
-    static constexpr int BOX_BYTES = ROW_BYTES < 128 ? ROW_BYTES : 128;   // inner extent of a TMA box
-    static constexpr int BOXES = ROW_BYTES / BOX_BYTES;
-    static constexpr int TILE_BYTES = UNIT * ROW_BYTES;                   // K or V of a unit
-    static constexpr int STAGE = 2 * TILE_BYTES;
-    // 128 KB of units, a power of two of them; of the largest ones as many as fit
-    static constexpr int NST = STAGE == 32 * 1024 ? 5 : 128 * 1024 / STAGE;
-    static_assert(NST * STAGE <= RING_BYTES, "ring");
+struct Cfg : UnitRing<D, E4M3> {
     static constexpr int MERGE_ROW = D + MERGE_LD;
     static constexpr int MERGE_BYTES = (CW / 2) * 16 * (MERGE_ROW + 2) * 4;
-    static constexpr int SMEM = NST * STAGE + MERGE_BYTES + 1024;
+    static constexpr int SMEM = Cfg::NST * Cfg::STAGE + MERGE_BYTES + 1024;
 };
 
-// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of one head:
-// boxes of [64 rows][128 or 64 bytes], swizzled as the tensor map says.
-template <int BOX_BYTES>
-__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
-    if (BOX_BYTES == 128)
-        return (uint32_t)((chunk >> 3) * (UNIT * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-    return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t *r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t *r, uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-template <bool F16>
-__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    if (F16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-    if (F16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
 template <bool B>
 struct Bool {
     static constexpr bool value = B;
@@ -144,50 +93,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp >= CW) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOAD));
         if (warp != CW) return;
-        // ---- producer: one unit = one page, K and V of one head ----
-        uint32_t it = 0;
-        bool ok = true;
-        while (ok && next_segment<UNIT>(p, cur, g)) {
-            const int hi_unit = (g.x.key_hi + UNIT - 1) / UNIT;
-            for (int u = g.u_begin; ok && u < g.u_end; u += 32) {
-                // page ids of the next 32 units, one a lane
-                int page = p.pg.num_pages;  // outside the map: reads as zeros
-                const int lp = g.x.u0 + u + lane;
-                if (u + lane < g.u_end && lp < hi_unit) {
-                    const int id = lp < p.pg.max_blocks ? p.pg.block_table[(int64_t)g.b * p.pg.max_blocks + lp] : -1;
-                    if (id >= 0 && id < p.pg.num_pages)
-                        page = id;
-                    else
-                        record_error(p.err, DSA_DEVERR_PAGE);
-                }
-                const int cnt = min(32, g.u_end - u);
-                for (int i = 0; i < cnt; ++i, ++it) {
-                    const int pg = __shfl_sync(0xffffffffu, page, i);
-                    const int s = it % C::NST;
-                    if (it >= C::NST) ok = mbar_wait(&empty[s], ((it / C::NST) - 1) & 1, p.err, &abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        uint8_t *st = ring + s * C::STAGE;
-                        mbar_expect_tx(&full[s], C::STAGE);
-#pragma unroll
-                        for (int x = 0; x < C::BOXES; ++x) {
-                            const int col = x * (C::BOX_BYTES / C::ELEM);
-                            tma_load_4d(st + x * UNIT * C::BOX_BYTES, &kmap, &full[s], col, 0, g.h, pg);
-                            tma_load_4d(st + C::TILE_BYTES + x * UNIT * C::BOX_BYTES, &vmap, &full[s], col, 0, g.h, pg);
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-        // copies in flight end before the block's shared memory does (after an
-        // abandoned run; otherwise the consumers have waited for them all)
-        if (!ok)
-            for (uint32_t j = it > C::NST ? it - C::NST : 0; j < it; ++j)
-                mbar_wait(&full[j % C::NST], (j / C::NST) & 1, p.err, nullptr);
+        load_units<C>(kmap, vmap, p, cur, ring, full, empty, &abort_flag);
         return;
     }
 
@@ -558,11 +464,15 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
     if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Rows of a tile: enough 16-row groups for one sequence's packed rows, up to 128.
-int tile_groups(int64_t max_rows) {
+// Rows of a tile: enough 16-row groups for one sequence's packed rows, up to
+// 128; up to eight rows over an 8-bit cache have a kernel of their own, in which
+// they are columns (33 sequences, one token of 8 heads a K/V head: EIGHT_US
+// against 285 us here).
+int tile_rows(int64_t max_rows, bool e4m3) {
+    if (e4m3 && max_rows <= 8) return 8;
     int mt = 1;
     while (mt < CW && mt * 16 < max_rows) mt *= 2;
-    return mt;
+    return 16 * mt;
 }
 
 struct Plan {
@@ -638,6 +548,8 @@ dsa_status launch_kw(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, c
 // row group's eight slots would then hold four units of a five-unit ring (16 rows, 2-byte cache, D = 128), 16.
 template <int D, bool IO_F16, bool E4M3>
 dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    if constexpr (E4M3)
+        if (p.TM == 8) return launch_paged_attn8(a, p, nc, st);
     if constexpr (Cfg<D, E4M3>::NST < 8)
         if (p.TM == 16) return launch_kw<D, IO_F16, E4M3, 16>(a, p, nc, st);
     return launch_kw<D, IO_F16, E4M3, 32>(a, p, nc, st);
@@ -667,7 +579,7 @@ bool paged_kv_maps(const dsa_kv_cache &c, int num_pages, CUtensorMap *km, CUtens
 size_t paged_attn_workspace_bytes(int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, bool e4m3, int32_t max_q,
                                   int32_t max_len, int32_t window, int sm_count) {
     const int G = H / Hkv;
-    size_t need = make_plan(16 * tile_groups((int64_t)max_q * G), UNIT, num_seqs, G, Hkv, D, max_q, max_len, window,
+    size_t need = make_plan(tile_rows((int64_t)max_q * G, e4m3), UNIT, num_seqs, G, Hkv, D, max_q, max_len, window,
                             sm_count).total;
     if (tc_shape(G, max_q, e4m3)) {  // (the call's scale and strides decide between the two)
         const size_t tc =
@@ -683,7 +595,7 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     const dsa_kv_cache &c = *a.cache;
     const int H = a.q.heads, D = c.Dk, G = H / c.heads;
     const bool tc = tc_shape(G, a.max_q, c.dtype == DSA_E4M3) && tc_call(a);
-    const Plan pl = make_plan(tc ? paged_attn_tc_rows(G) : 16 * tile_groups((int64_t)a.max_q * G), tc ? 128 : UNIT,
+    const Plan pl = make_plan(tc ? paged_attn_tc_rows(G) : tile_rows((int64_t)a.max_q * G, c.dtype == DSA_E4M3), tc ? 128 : UNIT,
                               a.pg.num_seqs, G, c.heads, D, a.max_q, a.max_len, a.window, dev->sm_count);
     if (!a.ws || a.ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(a.ws) & 255u)) return DSA_ERR_WORKSPACE;
     const bool e4m3 = c.dtype == DSA_E4M3;

@@ -90,7 +90,8 @@ def test_attention(L, lens, new, H, Hkv, D, dtype, cdt):  # noqa: F811
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 129, 1000, 2 ** 31 - 1])
 @pytest.mark.parametrize("lens,new,H,Hkv,D,cdt", [([700, 64, 1], [1, 1, 1], 8, 2, 128, None),
                                                   ([700, 64, 90], [300, 64, 3], 6, 2, 128, None),
-                                                  ([515, 140], [200, 1], 4, 4, 64, E4M3)])
+                                                  ([515, 140], [200, 1], 4, 4, 64, E4M3),
+                                                  ([700, 64, 1], [2, 1, 1], 8, 2, 128, E4M3)])
 def test_window(L, lens, new, H, Hkv, D, cdt, window):  # noqa: F811
     c = Case(L, lens, new, H, Hkv, D, BF16, cdt)
     c.check(*c.run(window), window)
@@ -260,11 +261,12 @@ def test_many_sequences(L):  # noqa: F811
             ref.assert_attended(out[at:at + m], c.ref(b), lse[at:at + m])
 
 
-@pytest.mark.parametrize("D,cdt,new", [(128, BF16, 1), (128, E4M3, 1), (64, BF16, 4), (128, BF16, 20)])
-def test_long_streams(L, D, cdt, new):  # noqa: F811
+@pytest.mark.parametrize("D,cdt,new,H", [(128, BF16, 1, 16), (128, E4M3, 1, 16), (64, E4M3, 1, 40), (64, BF16, 4, 16),
+                                         (128, BF16, 20, 16), (128, E4M3, 4, 24), (128, E4M3, 1, 64)])
+def test_long_streams(L, D, cdt, new, H):  # noqa: F811
     """Hundreds of units through each CTA's ring, over gigabytes of cache."""
     lens = [8192 + 1777 * (b % 7) for b in range(48)]
-    c = Case(L, lens, [new] * 48, 16, 8, D, BF16, cdt)
+    c = Case(L, lens, [new] * 48, H, 8, D, BF16, cdt)
     out, lse = c.run()
     no_error(L)
     for b in (0, 1, 13, 29, 46, 47):
