@@ -17,9 +17,9 @@
 // values, and the rows of q are scaled by a power of two to fit fp16 exactly.
 //
 // Measured: 64 sequences of 4096-65536 positions, one token each, 64 heads of
-// 128 on 8, bf16: 1256-1330 us for 8.95 GB (the measured copy rate); 33
-// sequences over an E4M3 cache 285-309 us for 1.43 GB (71-77% of it: twice the
-// instructions a byte); one token over 4097 positions 15 us on the device.
+// 128 on 8, bf16: 1230 us for 8.95 GB (above the measured copy rate, which has
+// writes in it); four drafts of 8 sequences 605 us; one token over 4097
+// positions 15 us on the device.
 #include <cuda_fp16.h>
 
 #include "dsa_device.cuh"
@@ -405,14 +405,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
     if (!rec.valid) return;
     const int r = blockIdx.y * JOIN_WARPS + warp_id();
     if (r >= rec.rows) return;
-    const Line line(rec.total, nc);
-    const int last = min(line.next(rec.end), nc);  // pieces: slot 1 of c, slot 0 of c + 1 .. last - 1
-    auto at = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * p.TM + r; };
+    const int parts = line_parts(p, nc), part = line_part(p, c);
+    const Line line(rec.total, parts);
+    const int last = min(line.next(rec.end), parts);  // pieces: slot 1 of this part, slot 0 of the next ones before `last`
+    const int stride = p.locked ? p.Hkv : 1;          // from a part's CTA to the next one's
+    auto at = [&](int i) { return ((int64_t)(c + (i - part) * stride) * 2 + (i == part ? 1 : 0)) * p.TM + r; };
     constexpr int V = D / 32;
     float acc[V], sum = 0.f, mx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    for (int base = c; base < last; base += 32) {  // 32 pieces at a time, a lane each for their weights
+    for (int base = part; base < last; base += 32) {  // 32 pieces at a time, a lane each for their weights
         const int mine = base + lane, cnt = min(32, last - base);
         float o[8][V];
         auto load = [&](int i0) {  // eight rows in flight, the first before their weights are known
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
             }
         };
         load(0);
-        const float ls = mine < last && (mine == c || line.start(mine) < line.start(mine + 1)) ? p.part_l[at(mine)] : -INFINITY;
+        const float ls = mine < last && (mine == part || line.start(mine) < line.start(mine + 1)) ? p.part_l[at(mine)] : -INFINITY;
         float top = ls;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -466,8 +468,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
 
 // Rows of a tile: enough 16-row groups for one sequence's packed rows, up to
 // 128; up to eight rows over an 8-bit cache have a kernel of their own, in which
-// they are columns (33 sequences, one token of 8 heads a K/V head: EIGHT_US
-// against 285 us here).
+// they are columns (33 sequences of 1000-40000 positions, one token of 8 heads a
+// K/V head: 252 us, 268 in long runs, against 257 and 287 as half of a 16-row tile).
 int tile_rows(int64_t max_rows, bool e4m3) {
     if (e4m3 && max_rows <= 8) return 8;
     int mt = 1;
@@ -559,7 +561,7 @@ template <int D, bool IO_F16>
 dsa_status launch_join(const PagedAttnParams &p, int nc, cudaStream_t st) {
     if (nc == 1) return DSA_OK;  // one CTA holds every tile whole
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(nc - 1, (p.TM + JOIN_WARPS - 1) / JOIN_WARPS);
+    cfg.gridDim = dim3(nc, (p.TM + JOIN_WARPS - 1) / JOIN_WARPS);
     cfg.blockDim = dim3(JOIN_WARPS * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -606,6 +608,12 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     p.T = a.T, p.H = H, p.Hkv = c.heads, p.G = G, p.TM = pl.TM;
     p.by_G = FastDiv::of(G), p.by_TM = FastDiv::of(pl.TM);
     p.max_q = a.max_q, p.max_len = a.max_len, p.window = a.window;
+    // Heads in step, where that idles no more than one CTA in twenty: 64 sequences' decode 1230 us against 1280,
+    // an 8-bit cache 252 against 284, drafts 605 against 630.  Chunks, whose keys come from L2, were slower (1658
+    // against 1634).
+    const int even = pl.nc / c.heads * c.heads;
+    p.locked = !tc && c.heads > 1 && even * 20 >= pl.nc * 19;
+    const int nc = p.locked ? even : pl.nc;
     p.scale_log2 = (float)(a.sm_scale * 1.4426950408889634 / (e4m3 ? c.k_scale : 1.f));
     p.v_inv = e4m3 ? 1.f / c.v_scale : 1.f;
     p.out = a.out, p.lse = a.lse;
@@ -615,15 +623,15 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     p.err = dev->err;
     const bool f16 = a.dtype == DSA_F16;
     dsa_status s;
-#define DSA_PAGED(D_)                                                                        (f16 ? (e4m3 ? launch<D_, true, true>(a, p, pl.nc, st) : launch<D_, true, false>(a, p, pl.nc, st))          : (e4m3 ? launch<D_, false, true>(a, p, pl.nc, st) : launch<D_, false, false>(a, p, pl.nc, st)))
+#define DSA_PAGED(D_)                                                                        (f16 ? (e4m3 ? launch<D_, true, true>(a, p, nc, st) : launch<D_, true, false>(a, p, nc, st))          : (e4m3 ? launch<D_, false, true>(a, p, nc, st) : launch<D_, false, false>(a, p, nc, st)))
     if (tc)
-        s = launch_paged_attn_tc(a, p, pl.nc, st);
+        s = launch_paged_attn_tc(a, p, nc, st);
     else
         s = D == 128 ? DSA_PAGED(128) : DSA_PAGED(64);
 #undef DSA_PAGED
     if (s != DSA_OK) return s;
-    if (D == 128) return f16 ? launch_join<128, true>(p, pl.nc, st) : launch_join<128, false>(p, pl.nc, st);
-    return f16 ? launch_join<64, true>(p, pl.nc, st) : launch_join<64, false>(p, pl.nc, st);
+    if (D == 128) return f16 ? launch_join<128, true>(p, nc, st) : launch_join<128, false>(p, nc, st);
+    return f16 ? launch_join<64, true>(p, nc, st) : launch_join<64, false>(p, nc, st);
 }
 
 }  // namespace dsa

@@ -10,7 +10,10 @@
 // many CTAs as it takes.  A CTA that holds a tile whole writes its rows;
 // pieces of a tile go to the workspace (at most two per CTA: one that began
 // in an earlier CTA, one that goes on in the next) and are joined by a second
-// kernel in the order of the line.  Lengths are read on the device: every CTA
+// kernel in the order of the line.  Where the heads divide the CTAs (`locked`),
+// every head has a line of its own and the CTAs of one part of all of them read
+// the same pages at the same time, so that the rows of a page, which lie
+// interleaved by heads, come from memory together.  Lengths are read on the device: every CTA
 // sums the units itself (a few thousand instructions at most), and its result
 // depends on nothing but the lengths.
 #pragma once
@@ -26,6 +29,7 @@ struct PagedAttnParams {
     const int32_t *q_start;
     PagedDev pg;
     int32_t T, H, Hkv, G, TM;  // T H < 2^31
+    int32_t locked;            // a line a head: CTA c is part c / Hkv of head c % Hkv
     FastDiv by_G, by_TM;
     int32_t max_q, max_len, window;
     float scale_log2;  // sm_scale * log2(e) (and 1 / k_scale)
@@ -96,7 +100,7 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {  // a >= 0, b >
     if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
     return a / b;
 }
-// The line's parts: the first `more` CTAs have per + 1 units, the others per.
+// A line's parts: the first `more` have per + 1 units, the others per.
 struct Line {
     int64_t per;
     int more;
@@ -105,13 +109,17 @@ struct Line {
         more = (int)(total - per * nc);
     }
     __device__ __forceinline__ int64_t start(int c) const { return per * c + min(c, more); }
-    // the first CTA that begins at or behind `at`
+    // the first part that begins at or behind `at`
     __device__ __forceinline__ int next(int64_t at) const {
         const int64_t big = (per + 1) * more;
         if (at <= big) return (int)div64(at + per, per + 1);
         return more + (int)(per > 0 ? div64(at - big + per - 1, per) : 0);
     }
 };
+
+// How many parts a line has, and which one CTA c of nc holds.
+__device__ __forceinline__ int line_parts(const PagedAttnParams &p, int nc) { return p.locked ? nc / p.Hkv : nc; }
+__device__ __forceinline__ int line_part(const PagedAttnParams &p, int c) { return p.locked ? c / p.Hkv : c; }
 
 struct Cursor {
     int b, h, t, u;   // sequence, K/V head, tile, unit of the tile
@@ -133,6 +141,8 @@ __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &
     const int lane = lane_id(), warp = warp_id(), nw = blockDim.x >> 5;
     const int B = p.pg.num_seqs;
     const bool single = (int64_t)p.max_q * p.G <= p.TM;  // one tile a sequence at most
+    const int lines = p.locked ? 1 : p.Hkv;              // heads on this CTA's line
+    const int head = p.locked ? c % p.Hkv : 0, parts = line_parts(p, nc), part = line_part(p, c);
     if (single && B <= 32) {
         // small batches of single tokens, where the plan's latency counts: every warp by itself, a lane a sequence
         int64_t per_head = 0;
@@ -140,7 +150,7 @@ __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &
             const SeqInfo s = seq_info(p, lane, c == 0 && warp == 0);
             if (s.n) per_head = tile_info<UNIT>(p, s, 0).nu;
         }
-        const int64_t w = per_head * p.Hkv;
+        const int64_t w = per_head * lines;
         int64_t inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -148,15 +158,16 @@ __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &
             if (lane >= o) inc += v;
         }
         const int64_t total = __shfl_sync(0xffffffffu, inc, 31);
-        const Line line(total, nc);
-        Cursor cur{0, 0, 0, 0, line.start(c), line.start(c + 1), total};
+        const Line line(total, parts);
+        Cursor cur{0, head, 0, 0, line.start(part), line.start(part + 1), total};
         const uint32_t past = __ballot_sync(0xffffffffu, inc > cur.at);
         if (cur.at < cur.end && past) {
             cur.b = __ffs(past) - 1;
             const int64_t off = cur.at - __shfl_sync(0xffffffffu, inc - w, cur.b);
             const int64_t ph = __shfl_sync(0xffffffffu, per_head, cur.b);
-            cur.h = (int)div64(off, ph);
-            cur.u = (int)(off - cur.h * ph);
+            const int h = (int)div64(off, ph);
+            cur.h += h;
+            cur.u = (int)(off - h * ph);
         }
         __syncthreads();
         return cur;
@@ -190,14 +201,14 @@ __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &
             for (int i = lane; i < cnt; i += 32) sum += sh.units[i];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) sh.total += sum * p.Hkv;
+            if (lane == 0) sh.total += sum * lines;
         }
         __syncthreads();
     }
     const int64_t total = sh.total;
-    const Line line(total, nc);
-    const int64_t begin = line.start(c), end = line.start(c + 1);
-    if (threadIdx.x == 0) sh.cur = Cursor{0, 0, 0, 0, begin, end, total};
+    const Line line(total, parts);
+    const int64_t begin = line.start(part), end = line.start(part + 1);
+    if (threadIdx.x == 0) sh.cur = Cursor{0, head, 0, 0, begin, end, total};
     __syncthreads();
     if (begin >= end) return sh.cur;
     int64_t before = 0;  // warp 0: units before the group of 32 sequences looked at
@@ -205,7 +216,7 @@ __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &
         const int cnt = B > PLAN_SEQS ? fill(base, false) : B;
         if (warp == 0) {
             for (int g = 0; g < cnt; g += 32) {
-                const int64_t w = g + lane < cnt ? sh.units[g + lane] * p.Hkv : 0;
+                const int64_t w = g + lane < cnt ? sh.units[g + lane] * lines : 0;
                 int64_t inc = w;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -235,7 +246,7 @@ __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &
                         if (tp) {
                             const int tl = __ffs(tp) - 1;
                             if (lane == tl) {
-                                sh.cur.b = b, sh.cur.h = h, sh.cur.t = t0 + tl;
+                                sh.cur.b = b, sh.cur.h = head + h, sh.cur.t = t0 + tl;
                                 sh.cur.u = (int)(off - sum - (ti - nu));
                                 sh.found = 1;
                             }
@@ -273,8 +284,8 @@ __device__ __forceinline__ bool next_segment(const PagedAttnParams &p, Cursor &c
     int nt = seq_tiles(p, g.s);
     while (c.t >= nt) {  // the cursor stands behind a head's last tile, or at a sequence without rows
         c.t = 0;
-        if (nt == 0 || ++c.h == p.Hkv) {
-            c.h = 0;
+        if (nt == 0 || p.locked || ++c.h == p.Hkv) {
+            if (!p.locked) c.h = 0;
             if (++c.b >= p.pg.num_seqs) return false;  // the lengths changed under the call
             g.s = seq_info(p, c.b);
             nt = seq_tiles(p, g.s);
