@@ -577,11 +577,11 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
     if (cache->dtype != DSA_E4M3 && cache->dtype != dtype) return DSA_ERR_INVALID_ARG;
     if (rope)
         if (dsa_status s = rope_spec_check(rope, cache->Dk)) return s;
+    if (n == 0) return DSA_OK;  // (an empty array may have no address)
     if ((q != nullptr) != (H > 0) || (q && (!rope || !q_out))) return DSA_ERR_INVALID_ARG;
     if (q && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
         return DSA_ERR_INVALID_ARG;
     if ((v_new != nullptr) != (cache->v != nullptr)) return DSA_ERR_INVALID_ARG;
-    if (n == 0) return DSA_OK;
     if (!k_new || !tok_seq || !tok_pos) return DSA_ERR_INVALID_ARG;
     AppendRopeArgs a{{k_new, k_token_stride, k_head_stride, cache->heads},
                      {v_new, v_token_stride, v_head_stride, v_new ? cache->heads : 0},
@@ -617,7 +617,7 @@ dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_
     if (T == 0) return DSA_OK;
     // positions, and their differences to a window's, stay within 32 bits
     constexpr int32_t most = 1 << 30;
-    if (T > most || max_q > most || max_len > most || (int64_t)T * H >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    if (T > most || max_q > most || max_len > most || (int64_t)T * H >= ((int64_t)1 << 31) - 512) return DSA_ERR_UNSUPPORTED;
     if (window >= max_len) window = 0;  // all of it is within the window
     if (!q || !out || !aligned16(q) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     if ((T > 1 && (q_token_stride & 7)) || (H > 1 && (q_head_stride & 7))) return DSA_ERR_INVALID_ARG;

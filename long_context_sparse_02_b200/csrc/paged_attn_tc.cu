@@ -98,19 +98,23 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // A stream's rows of a tile, and the segment's units that they see ([lo, hi), of the tile's units).
 struct Stream {
-    int rows, lo, hi;
+    int first, rows;  // of its row block: rows first .. rows - 1 are there
+    int lo, hi;
+    int tok0;         // the new token of its row 0 (below 0: not there)
     int p_first, p_last, key_lo, key_hi;
 };
 __device__ __forceinline__ Stream stream_info(const PagedAttnParams &p, const Segment &g, int st) {
     Stream s;
-    const int rs = p.TM / 2, r0 = g.x.row0 + st * rs;
-    s.rows = min(max(g.x.rows - st * rs, 0), rs);
+    const int rs = p.TM / 2, r0 = g.x.base + st * rs, past = g.s.L - g.s.n;
+    const int begin = max(r0, 0), end = min(r0 + rs, g.s.n * p.G);  // packed rows (whole tokens)
+    s.first = begin - r0, s.rows = end - r0;
     s.lo = s.hi = g.u_begin;
-    s.p_first = g.s.L - g.s.n + p.by_G.div(r0);
-    s.p_last = s.p_first + p.by_G.div(s.rows) - 1;  // rows are whole tokens
+    s.tok0 = p.by_G.div(g.t * p.TM + st * rs) - p.by_G.div(g.s.shift);
+    s.p_first = past + max(s.tok0, 0);
+    s.p_last = past + s.tok0 + (s.rows > 0 ? p.by_G.div(s.rows) - 1 : -1);
     s.key_hi = max(s.p_last + 1, 0);
     s.key_lo = p.window ? max(s.p_first - p.window + 1, 0) : 0;
-    if (s.rows > 0 && s.key_hi > s.key_lo) {
+    if (s.rows > s.first && s.key_hi > s.key_lo) {
         s.lo = max(s.key_lo / UNIT - g.x.u0, g.u_begin);
         s.hi = max(min((s.key_hi + UNIT - 1) / UNIT - g.x.u0, g.u_end), s.lo);
     }
@@ -121,7 +125,7 @@ __device__ __forceinline__ Stream stream_info(const PagedAttnParams &p, const Se
 struct Walk {
     Cursor cur;
     int64_t end;
-    int h, whole, slot, row0, q0, tile_row0, tile_rows;
+    int h, whole, slot, row0, piece0, q0, tile_row0, tile_rows;
 };
 
 // 32 scores to weights 2^(c s - mc), rounded to the values' type and packed into out[0..15]; the sum of the
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
                                 ok = __all_sync(0xffffffffu, ok);
                                 if (!ok) break;
                                 if (lane == 0) {
-                                    const int tok = g.s.q0 + p.by_G.div(g.x.row0 + st * (p.TM / 2));
+                                    const int tok = g.s.q0 + s.tok0;  // (below 0: zeros)
                                     mbar_expect_tx(&q_full[st], (p.TM / 2) * 128 * C::NH);
 #pragma unroll
                                     for (int x = 0; x < C::NH; ++x)
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
         if (lane == 0) wk.cur = cur;
         __syncwarp();
         while (ok) {
-            int i, hi, key0, p_first, pos, p_min, p_max;  // (p_min .. p_max: of the warp's rows)
+            int i, hi, key0, pos, p_min, p_max;  // (p_min .. p_max: of the warp's rows)
             bool have;
             {
                 Cursor cu = wk.cur;
@@ -615,16 +619,17 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
                 __syncwarp();
                 if (!more) break;
                 const Stream s = stream_info(p, g, st);
-                have = r < s.rows;
-                pos = have ? s.p_first + tok : -1;
-                p_min = s.p_first + p.by_G.div(r & ~31), p_max = min(s.p_first + p.by_G.div(r | 31), s.p_last);
-                i = s.lo, hi = s.hi, key0 = (g.x.u0 + s.lo) * UNIT, p_first = s.p_first;
+                const int p0 = g.s.L - g.s.n + s.tok0;  // of row 0
+                have = r >= s.first && r < s.rows;
+                pos = have ? p0 + tok : -1;
+                p_min = max(p0 + p.by_G.div(r & ~31), s.p_first), p_max = min(p0 + p.by_G.div(r | 31), s.p_last);
+                i = s.lo, hi = s.hi, key0 = (g.x.u0 + s.lo) * UNIT;
                 if (lane == 0) {
                     wk.cur = cu;
                     wk.end = cu.at - (g.u_end - g.u_begin) + g.x.nu;
                     wk.h = g.h, wk.q0 = g.s.q0, wk.tile_row0 = g.x.row0, wk.tile_rows = g.x.rows;
                     wk.whole = g.whole(), wk.slot = g.slot();
-                    wk.row0 = g.s.q0 - (g.s.L - g.s.n);
+                    wk.row0 = g.s.q0 + s.tok0, wk.piece0 = g.x.base - g.x.row0 + st * (p.TM / 2);
                 }
                 __syncwarp();
             }
@@ -656,8 +661,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
             const bool whole = wk.whole;
             const float inv = l > 0.f ? p.v_inv / l : 0.f;
             const float ls = l > 0.f ? m * c + log2f(l) : -INFINITY;
-            const int64_t orow = (int64_t)(wk.row0 + p_first + tok) * p.H + wk.h * p.G + (r - tok * p.G);
-            const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + st * (p.TM / 2) + r;
+            const int64_t orow = (int64_t)(wk.row0 + tok) * p.H + wk.h * p.G + (r - tok * p.G);
+            const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + wk.piece0 + r;
             if (have) {
                 if (!whole)
                     p.part_l[piece] = ls;

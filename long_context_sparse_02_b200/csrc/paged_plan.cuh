@@ -2,7 +2,9 @@
 //
 // A tile is TM packed rows of one sequence and one K/V head: row r is query
 // head (r % G) of the group and the sequence's new token r / G, so all query
-// heads that share a K/V head share its loads.  Its work is the run of units
+// heads that share a K/V head share its loads.  (Within a window, chunks' tiles
+// may begin at multiples of `align` positions, a sequence's first tile having
+// fewer rows: a row block then touches one key unit less, more often than not.)  Its work is the run of units
 // (UNIT consecutive key positions, aligned) that its rows see.  All tiles'
 // units, in the order sequence, head, tile, unit, form one line, which is cut
 // into equal parts, one per CTA: whatever the mix of lengths, every CTA gets
@@ -28,7 +30,8 @@ struct PagedAttnParams {
     int64_t q_token, q_head;
     const int32_t *q_start;
     PagedDev pg;
-    int32_t T, H, Hkv, G, TM;  // T H < 2^31
+    int32_t T, H, Hkv, G, TM;  // T H < 2^31 - 512
+    int32_t align;             // tokens; 0: a tile begins wherever the last one ended
     int32_t locked;            // a line a head: CTA c is part c / Hkv of head c % Hkv
     FastDiv by_G, by_TM;
     int32_t max_q, max_len, window;
@@ -50,6 +53,7 @@ struct PieceRec {
 
 struct SeqInfo {
     int n, L, q0;  // new tokens, length, first row of q
+    int shift;     // packed rows that the first tile goes without
 };
 __device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams &p, int b, bool report = false) {
     SeqInfo s;
@@ -69,11 +73,13 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams &p, int b, boo
         if (report) record_error(p.err, bad);
         s.n = 0;
     }
+    s.shift = p.align && s.L > s.n ? (s.L - s.n) % p.align * p.G : 0;
     return s;
 }
 
 struct Tile {
     int row0, rows;        // packed rows
+    int base;              // where they would begin without a shift's limit (at most row0)
     int p_first, p_last;   // positions of its first and last token (below 0: no such position)
     int key_lo, key_hi;    // positions that some row sees
     int u0, nu;            // units
@@ -82,8 +88,9 @@ template <int UNIT>
 __device__ __forceinline__ Tile tile_info(const PagedAttnParams &p, const SeqInfo &s, int t) {
     Tile x;
     const int total = s.n * p.G;
-    x.row0 = t * p.TM;
-    x.rows = min(p.TM, total - x.row0);
+    x.base = t * p.TM - s.shift;
+    x.row0 = max(x.base, 0);
+    x.rows = min(x.base + p.TM, total) - x.row0;
     x.p_first = s.L - s.n + p.by_G.div(x.row0);
     x.p_last = s.L - s.n + p.by_G.div(x.row0 + x.rows - 1);
     x.key_hi = max(x.p_last + 1, 0);
@@ -93,7 +100,7 @@ __device__ __forceinline__ Tile tile_info(const PagedAttnParams &p, const SeqInf
     return x;
 }
 __device__ __forceinline__ int seq_tiles(const PagedAttnParams &p, const SeqInfo &s) {
-    return s.n ? p.by_TM.div(s.n * p.G - 1) + 1 : 0;
+    return s.n ? p.by_TM.div(s.n * p.G + s.shift - 1) + 1 : 0;
 }
 
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {  // a >= 0, b > 0; short where both are
@@ -140,7 +147,7 @@ template <int UNIT>
 __device__ Cursor plan_cta(const PagedAttnParams &p, int c, int nc, PlanShared &sh) {
     const int lane = lane_id(), warp = warp_id(), nw = blockDim.x >> 5;
     const int B = p.pg.num_seqs;
-    const bool single = (int64_t)p.max_q * p.G <= p.TM;  // one tile a sequence at most
+    const bool single = ((int64_t)p.max_q + p.align) * p.G <= p.TM;  // one tile a sequence at most
     const int lines = p.locked ? 1 : p.Hkv;              // heads on this CTA's line
     const int head = p.locked ? c % p.Hkv : 0, parts = line_parts(p, nc), part = line_part(p, c);
     if (single && B <= 32) {

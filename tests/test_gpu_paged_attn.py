@@ -97,6 +97,46 @@ def test_window(L, lens, new, H, Hkv, D, cdt, window):  # noqa: F811
     c.check(*c.run(window), window)
 
 
+@pytest.mark.parametrize("n,m", [(255, 128), (256, 128), (257, 257), (700, 573), (700, 572), (1000, 1), (300, 299), (130, 131)])
+def test_window_of_aligned_tiles(L, n, m):  # noqa: F811
+    """Chunks that begin on, before and behind a multiple of 128, from the sequence's start and from before it."""
+    c = Case(L, [n, 200], [m, 150], 3, 3, 128)
+    c.check(*c.run(128), 128)
+
+
+def test_no_tokens(L):  # noqa: F811
+    """Calls of no tokens return empty results and launch nothing."""
+    c = Case(L, [64], [1], 4, 2, 64)
+    freq = L.rope_frequencies(64)[0].cuda()
+    none = torch.empty(0, device="cuda", dtype=torch.int32)
+    q, kv = torch.empty(0, 4, 64, device="cuda", dtype=BF16), torch.empty(0, 2, 64, device="cuda", dtype=BF16)
+    assert L.rope(q, none, L.rope_spec(freq), k=kv)[1].shape == (0, 2, 64)
+    assert L.append_rope(kv, kv, none, none, c.pg, c.cache, L.rope_spec(freq), q=q).shape == (0, 4, 64)
+    c.q_start.zero_()
+    out, lse = L.paged_attn(q, c.cache, c.pg, c.q_start, 1, 64, want_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    no_error(L)
+
+
+def test_two_graphs_share_a_workspace(L):  # noqa: F811
+    """Two captured calls of different shapes on one workspace, replayed in turn."""
+    a, b = Case(L, [3000, 40], [1, 1], 16, 2, 128), Case(L, [500, 900], [200, 3], 16, 2, 128, seed=3)
+    ws = L.paged_attn_workspace(203, 16, b.cache, b.pg, 200, 3000)
+    outs, graphs = [], []
+    for c in (a, b):
+        c.run(ws=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.run(ws=ws))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for c, (out, lse) in zip((a, b), outs):
+        c.check(out, lse)
+
+
 @pytest.mark.parametrize("cdt", [None, E4M3])
 def test_cache_strides(L, cdt):  # noqa: F811
     """Heads before rows; keys and values as halves of one array; q a slice of a fused projection."""
