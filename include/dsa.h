@@ -458,8 +458,8 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  *            need no initialisation; calls that may overlap need one each
  * A page outside [0, num_pages) reads as zeros and sets DSA_DEVERR_PAGE.
  * Softmax statistics and sums are fp32; the softmax weights enter the second
- * product in the q type (fp16 for an E4M3 cache).  Results do not depend on
- * what else is in the call's timing: no atomics, a fixed order of sums.
+ * product in the q type (fp16 for an E4M3 cache).  The same call gives the same
+ * bits each time: no atomics, a fixed order of sums.
  * Supported: Dk == Dv in {64, 128}, H a multiple of heads; T, max_q, max_len up to
  * 2^30, T * H below 2^31 - 512. */
 size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, const dsa_kv_cache *cache,

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
         } else if (warp < MMA_WARP + 2) {
             // ---- matrix products: one thread.  What it does between two products is seen by the tensor pipe (its
             // queue is short), so it does little: descriptors differ in their start address alone (16-byte units
-            // in the low bits), ring positions are counted along, and values are cleared by another warp. ----
+            // in the low bits), ring positions are counted along, and other warps clear values or widen codes. ----
             if (elect_one()) {
                 constexpr uint32_t FMT = F16 ? 0 : 1;
                 constexpr uint32_t ID_S = idesc(FMT, FMT, 0, 0, UNIT, 128);
