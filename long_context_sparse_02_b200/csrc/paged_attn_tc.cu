@@ -602,7 +602,6 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
         const int st = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter: lane 32 x (warp % 4), bits 16 up
         const uint32_t ts = tmem + lanes + st * 128, to = tmem + lanes + C::O_COL + st * 128;
-        float c = p.scale_log2;
         uint32_t sn = 0, on = 0;  // S tiles and outputs waited for
         bool ok = true;
         // A row of scores needs 128 registers: the walk's state waits in shared memory meanwhile.
@@ -635,6 +634,10 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
             }
             const bool some = i < hi;
             float m = -INFINITY, l = 0.f;  // the reference that the weights refer to (raw scores), their sum
+            // A row of the block that is not there (nothing of the tile's, or what an earlier tile left in shared
+            // memory) has scores too: at a scale of 0 they move no reference, which the warp's rows move together,
+            // so that the others' bits do not depend on them.
+            float c = have ? p.scale_log2 : 0.f;
             for (bool first = true; i < hi; ++i, key0 += UNIT, first = false) {
                 ok = mbar_wait(&s_full[st], sn & 1, p.err, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
                 ++sn;
                 tc_fence_after();
                 // (the products that these scores come from waited for the row's fitting; `on` segments had any before)
-                if (FIT && first) c = p.scale_log2 * row_scale[on & 1][st][FIT ? r : 0];
+                if (FIT && first && have) c = p.scale_log2 * row_scale[on & 1][st][FIT ? r : 0];
                 if (key0 + UNIT - 1 <= p_min && (!p.window || key0 > p_max - p.window))
                     softmax_tile<D, F16>(ts, to, c, first, m, l);
                 else
