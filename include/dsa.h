@@ -458,7 +458,10 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  *            need no initialisation; calls that may overlap need one each
  * A page outside [0, num_pages) reads as zeros and sets DSA_DEVERR_PAGE.
  * Softmax statistics and sums are fp32; the softmax weights enter the second
- * product in the q type (fp16 for an E4M3 cache).  The same call gives the same
+ * product in the q type (fp16 for an E4M3 cache), one rounding each; of fp16
+ * ones, what lies 2^-36 below a row's largest is lost.  Over an E4M3 cache bf16
+ * rows of q enter the first product in fp16, times a power of two: what lies
+ * 2^-24 below the row's largest element is lost.  The same call gives the same
  * bits each time: no atomics, a fixed order of sums.
  * Supported: Dk == Dv in {64, 128}, H a multiple of heads; T, max_q, max_len up to
  * 2^30, T * H below 2^31 - 512. */

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                       const PagedAttnParams p, const int MT) {
     using C = Cfg<D, E4M3>;
     constexpr bool MM_F16 = IO_F16 || E4M3;
+    constexpr float LIFT = MM_F16 ? FP16_LIFT : 0.f;
     constexpr int KS = D / 16;  // k-steps of q.k; also pairs of 8-wide output tiles
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -213,8 +214,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < NT; ++i) x = fmaxf(x, fmaxf(s[i][2 * r], s[i][2 * r + 1]));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                mu[r] = x == -INFINITY ? 0.f : x;
-                f[r] = ex2_approx(m[r] - mu[r]);
+                const float top = x == -INFINITY ? 0.f : x;
+                f[r] = ex2_approx(m[r] - top);
+                mu[r] = top - LIFT;
                 m[r] = x;
             }
 #pragma unroll
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!have[r]) continue;
                 const int row = rbase + gid + 8 * r, tok = p.by_G.div(row), hg = row - tok * p.G;
                 const float inv = l[r] > 0.f ? p.v_inv / l[r] : 0.f;
-                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) : -INFINITY;
+                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) - LIFT : -INFINITY;
                 const int64_t orow = (int64_t)(g.s.q0 + tok) * p.H + g.h * p.G + hg;
                 const int trow = row - g.x.row0;
                 if (tig == 0) {

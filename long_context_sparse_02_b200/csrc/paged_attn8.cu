@@ -174,8 +174,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                mu[r] = x == -INFINITY ? 0.f : x;
-                f[r] = ex2_approx(m[r] - mu[r]);
+                const float top = x == -INFINITY ? 0.f : x;
+                f[r] = ex2_approx(m[r] - top);
+                mu[r] = top - FP16_LIFT;
                 m[r] = x;
             }
 #pragma unroll
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (row >= rows) continue;
                 const int tok = p.by_G.div(row), hg = row - tok * p.G;
                 const float inv = l[r] > 0.f ? p.v_inv / l[r] : 0.f;
-                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) : -INFINITY;
+                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) - FP16_LIFT : -INFINITY;
                 const int64_t orow = (int64_t)(g.s.q0 + tok) * p.H + g.h * p.G + hg;
                 if (gid == 0) {
                     if (!whole)

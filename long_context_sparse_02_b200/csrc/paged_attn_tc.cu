@@ -18,7 +18,8 @@
 // Tensor memory is full: S0 S1 O0 O1 at 128 columns each.  The running
 // maximum that the weights refer to is only moved when it has grown by more
 // than 2^8 (weights stay below 2^8, their sum is fp32, and the quotient does
-// not depend on the reference), so O is rarely rescaled.  Rows of q come by
+// not depend on the reference), so O is rarely rescaled.  fp16 weights, whose
+// range is short, are lifted by 2^11 and follow the maximum within 2^4.  Rows of q come by
 // tensor copies whose box is a row block; queries and scores never touch
 // registers before the softmax.
 //
@@ -96,6 +97,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// How far (in octaves) the maximum may outgrow the reference of the weights, and what the weights are lifted by: up to
+// 2^15 together, so that fp16's whole steps reach 25 octaves below the largest weight and its last ones 35; unlifted
+// they reached 14 and 24, and the many small weights of a long history under one large one were lost.
+template <bool F16>
+constexpr float LAG = F16 ? 4.f : 8.f;
+template <bool F16>
+constexpr float LIFT = F16 ? 11.f : 0.f;
+
 // A stream's rows of a tile, and the segment's units that they see ([lo, hi), of the tile's units).
 struct Stream {
     int first, rows;  // of its row block: rows first .. rows - 1 are there
@@ -128,8 +137,8 @@ struct Walk {
     int h, whole, slot, row0, piece0, q0, tile_row0, tile_rows;
 };
 
-// 32 scores to weights 2^(c s - mc), rounded to the values' type and packed into out[0..15]; the sum of the
-// unrounded ones.
+// 32 scores to weights 2^(c s - mc), mc being the scaled reference less the lift, rounded to the values' type and
+// packed into out[0..15]; the sum of the unrounded ones.
 template <bool F16>
 __device__ __forceinline__ float weigh(const uint32_t *v, uint32_t *out, float c, float mc) {
     const uint64_t c2 = pk(c, c), n2 = pk(-mc, -mc);
@@ -191,9 +200,9 @@ __device__ __forceinline__ Sight sight(int key0, int pos, int p_min, int p_max, 
 }
 
 // Moves the reference m to `top` if some row of the warp has outgrown it, and rescales what refers to it.
-template <int D>
+template <int D, bool F16>
 __device__ __forceinline__ void move_reference(uint32_t to, float c, float top, bool first, float &m, float &l) {
-    if (__any_sync(0xffffffffu, (top - m) * c > 8.f)) {  // (false where both are -inf)
+    if (__any_sync(0xffffffffu, (top - m) * c > LAG<F16>)) {  // (false where both are -inf)
         const float f = ex2_approx((m - (top == -INFINITY ? 0.f : top)) * c);
         m = top;
         l *= f;
@@ -220,8 +229,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
 #pragma unroll
     for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, v + 32 * x);
     tmem_wait_ld();
-    move_reference<D>(to, c, fmaxf(fmaxf(fmaxf(max32(v), max32(v + 32)), fmaxf(max32(v + 64), max32(v + 96))), m), first, m, l);
-    const float mc = m == -INFINITY ? 0.f : m * c;
+    const float top = fmaxf(fmaxf(max32(v), max32(v + 32)), fmaxf(max32(v + 64), max32(v + 96)));
+    move_reference<D, F16>(to, c, fmaxf(top, m), first, m, l);
+    const float mc = (m == -INFINITY ? 0.f : m * c) - LIFT<F16>;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         l += weigh<F16>(v + 32 * x, v + 16 * x, c, mc);
@@ -255,8 +265,8 @@ __device__ __forceinline__ void softmax_edge(uint32_t ts, uint32_t to, float c, 
         load(x);
         top = fmaxf(top, max32(v));
     }
-    move_reference<D>(to, c, top, first, m, l);
-    const float mc = m == -INFINITY ? 0.f : m * c;
+    move_reference<D, F16>(to, c, top, first, m, l);
+    const float mc = (m == -INFINITY ? 0.f : m * c) - LIFT<F16>;
 #pragma unroll 1
     for (int x = 0; x < 4; ++x) {
         if (see.none >> x & 1) {
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
             }
             const bool whole = wk.whole;
             const float inv = l > 0.f ? p.v_inv / l : 0.f;
-            const float ls = l > 0.f ? m * c + log2f(l) : -INFINITY;
+            const float ls = l > 0.f ? m * c + log2f(l) - LIFT<F16> : -INFINITY;
             const int64_t orow = (int64_t)(wk.row0 + tok) * p.H + wk.h * p.G + (r - tok * p.G);
             const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + wk.piece0 + r;
             if (have) {

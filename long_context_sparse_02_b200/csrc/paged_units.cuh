@@ -9,6 +9,12 @@ namespace dsa {
 
 constexpr int UNIT_KEYS = 64;  // a unit: one page of one head, keys and values
 
+// Softmax weights that are rounded to fp16 are taken as 2^(l - m + LIFT): at most 2^15 of fp16's 65504, so that fp16's
+// whole steps reach 29 octaves below the largest and its last ones 39.  At most 1 they reached 14 and 24, and the many
+// small weights of a long history under one large one were lost.  Their sum carries the same factor, which the quotient
+// does not see and the log-sum-exp takes out.
+constexpr float FP16_LIFT = 15.f;
+
 template <int D, bool E4M3>
 struct UnitRing {
     static constexpr int ELEM = E4M3 ? 1 : 2;
