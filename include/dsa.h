@@ -443,7 +443,9 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  * of 0 .. p); query head h reads K/V head h / (H / heads):
  *   l_s = sm_scale * q.k_s,  out = sum_s softmax(l)_s v_s,  lse = ln sum_s exp(l_s)
  * A query without any position (n_b > seq_lens[b], an empty sequence) gets
- * out = 0, lse = -inf.  Rows from q_start[num_seqs] on are left as they were.
+ * out = 0, lse = -inf.  A NaN in a query, or a score of +inf, makes that
+ * query's out and lse NaN, and no other's.  Rows from q_start[num_seqs] on are
+ * left as they were.
  *   q        device bf16 or fp16 (dtype): H heads of Dk, strides as in dsa_rope,
  *            multiples of 8, 16-byte aligned
  *   cache    bf16 or fp16 as q, or E4M3; rows at positions below seq_lens must be

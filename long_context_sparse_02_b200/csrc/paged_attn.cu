@@ -354,8 +354,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int r = 0; r < 2; ++r) {
                 if (!have[r]) continue;
                 const int row = rbase + gid + 8 * r, tok = p.by_G.div(row), hg = row - tok * p.G;
-                const float inv = l[r] > 0.f ? p.v_inv / l[r] : 0.f;
-                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) - LIFT : -INFINITY;
+                // (only a row that saw nothing has a sum of 0: a NaN goes on into the row's results)
+                const float inv = l[r] != 0.f ? p.v_inv / l[r] : 0.f;
+                const float ls = l[r] != 0.f ? m[r] + log2f(l[r]) - LIFT : -INFINITY;
                 const int64_t orow = (int64_t)(g.s.q0 + tok) * p.H + g.h * p.G + hg;
                 const int trow = row - g.x.row0;
                 if (tig == 0) {
@@ -439,7 +440,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         top = fmaxf(top, mx);
-        if (top == -INFINITY) continue;
+        const bool nan = __any_sync(0xffffffffu, isnan(ls));  // (which the maximum leaves out, and the weights do not)
+        if (top == -INFINITY) {
+            if (!nan) continue;
+            top = 0.f;
+        }
         const float f = ex2_approx(mx - top), w = ex2_approx(ls - top);
         mx = top;
         sum *= f;
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
-                if (i0 + i < cnt && wi > 0.f) {  // (a piece without weight may be unwritten)
+                if (i0 + i < cnt && wi != 0.f) {  // (a piece without weight may be unwritten)
                     sum += wi;
 #pragma unroll
                     for (int j = 0; j < V; ++j) acc[j] = fmaf(wi, o[i][j], acc[j]);
@@ -459,13 +464,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
             load(i0);
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const int row = rec.row0 + r, tok = p.by_G.div(row);
     const int64_t orow = (int64_t)(rec.q0 + tok) * p.H + rec.h * p.G + (row - tok * p.G);
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow * D + lane * V);
 #pragma unroll
     for (int j = 0; j < V; j += 2) dst[j / 2] = paged_pack2<IO_F16>(acc[j] * inv, acc[j + 1] * inv);
-    if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && lane == 0) p.lse[orow] = sum != 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Rows of a tile: enough 16-row groups for one sequence's packed rows, up to

@@ -279,8 +279,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int row = 2 * tig + r;
                 if (row >= rows) continue;
                 const int tok = p.by_G.div(row), hg = row - tok * p.G;
-                const float inv = l[r] > 0.f ? p.v_inv / l[r] : 0.f;
-                const float ls = l[r] > 0.f ? m[r] + log2f(l[r]) - FP16_LIFT : -INFINITY;
+                // (only a row that saw nothing has a sum of 0: a NaN goes on into the row's results)
+                const float inv = l[r] != 0.f ? p.v_inv / l[r] : 0.f;
+                const float ls = l[r] != 0.f ? m[r] + log2f(l[r]) - FP16_LIFT : -INFINITY;
                 const int64_t orow = (int64_t)(g.s.q0 + tok) * p.H + g.h * p.G + hg;
                 if (gid == 0) {
                     if (!whole)

@@ -672,8 +672,9 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
                 tc_fence_after();
             }
             const bool whole = wk.whole;
-            const float inv = l > 0.f ? p.v_inv / l : 0.f;
-            const float ls = l > 0.f ? m * c + log2f(l) - LIFT<F16> : -INFINITY;
+            // (only a row that saw nothing has a sum of 0: a NaN goes on into the row's results)
+            const float inv = l != 0.f ? p.v_inv / l : 0.f;
+            const float ls = l != 0.f ? m * c + log2f(l) - LIFT<F16> : -INFINITY;
             const int64_t orow = (int64_t)(wk.row0 + tok) * p.H + wk.h * p.G + (r - tok * p.G);
             const int64_t piece = ((int64_t)blockIdx.x * 2 + wk.slot) * p.TM + wk.piece0 + r;
             if (have) {
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
                     tmem_wait_ld();
                 }
 #pragma unroll
-                for (int q = 0; q < 32; ++q) o[q] = l > 0.f ? __float_as_uint(__uint_as_float(o[q]) * inv) : 0u;
+                for (int q = 0; q < 32; ++q) o[q] = l != 0.f ? __float_as_uint(__uint_as_float(o[q]) * inv) : 0u;
                 if (!have) continue;
                 if (whole) {
 #pragma unroll

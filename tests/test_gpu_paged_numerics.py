@@ -72,3 +72,21 @@ def test_concentrated_weights(L, dtype, cdt, G, new, depth):  # noqa: F811
         assert (err <= tol).all(), f"{float((err / want).max())} of the output"
         e = (lse[t].double() - torch.logsumexp(s[:m], 0)).abs()
         assert (e <= 2 * ds + 2.0 ** -21 * depth + 2.0 ** -17).all()
+
+
+@pytest.mark.parametrize("n", [300, 40000])
+@pytest.mark.parametrize("dtype,cdt,G,new", KERNELS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_queries_that_are_not_finite(L, dtype, cdt, G, new, n, bad):  # noqa: F811
+    """A query of NaN or infinity gives no number, whether its keys were split or not; the other rows are as ever."""
+    c = Case(L, [n], [new], G, 1, 128, dtype, cdt)
+    c.q[0, 1, 5] = bad
+    out, lse = c.run()
+    no_error(L)
+    assert not torch.isfinite(out[0, 1]).any() and not torch.isfinite(lse[0, 1])
+    if bad != bad:
+        assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    c.q[0, 1] = 0
+    r = [x.clone() for x in c.ref(0)]
+    out[0, 1], lse[0, 1] = r[0][0, 1].to(dtype), r[1][0, 1].float()
+    ref.assert_attended(out, tuple(r), lse, F16 if cdt else None)
