@@ -97,6 +97,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// A row's scale stays above 0, where the first maximum would not count as grown and the reference not leave -inf.  Only
+// 8-bit caches come near it (a division by their scale, and by the row's power of two), whose scores are below 2^33:
+// less than 2^-80 in octaves, and 0 either way.
+constexpr float MIN_SCALE = 1e-37f;
+
 // How far (in octaves) the maximum may outgrow the reference of the weights, and what the weights are lifted by: up to
 // 2^15 together, so that fp16's whole steps reach 25 octaves below the largest weight and its last ones 35; unlifted
 // they reached 14 and 24, and the many small weights of a long history under one large one were lost.
@@ -647,7 +652,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
             // A row of the block that is not there (nothing of the tile's, or what an earlier tile left in shared
             // memory) has scores too: at a scale of 0 they move no reference, which the warp's rows move together,
             // so that the others' bits do not depend on them.
-            float c = have ? p.scale_log2 : 0.f;
+            float c = have ? fmaxf(p.scale_log2, MIN_SCALE) : 0.f;
             for (bool first = true; i < hi; ++i, key0 += UNIT, first = false) {
                 ok = mbar_wait(&s_full[st], sn & 1, p.err, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3>::THREADS), 1)
                 ++sn;
                 tc_fence_after();
                 // (the products that these scores come from waited for the row's fitting; `on` segments had any before)
-                if (FIT && first && have) c = p.scale_log2 * row_scale[on & 1][st][FIT ? r : 0];
+                if (FIT && first && have) c = fmaxf(p.scale_log2 * row_scale[on & 1][st][FIT ? r : 0], MIN_SCALE);
                 if (key0 + UNIT - 1 <= p_min && (!p.window || key0 > p_max - p.window))
                     softmax_tile<D, F16>(ts, to, c, first, m, l);
                 else

@@ -90,3 +90,18 @@ def test_queries_that_are_not_finite(L, dtype, cdt, G, new, n, bad):  # noqa: F8
     r = [x.clone() for x in c.ref(0)]
     out[0, 1], lse[0, 1] = r[0][0, 1].to(dtype), r[1][0, 1].float()
     ref.assert_attended(out, tuple(r), lse, F16 if cdt else None)
+
+
+@pytest.mark.parametrize("new", [1, 2, 16])
+def test_tiny_queries_and_scales(L, new):  # noqa: F811
+    """Scores that vanish in fp32 weigh all keys alike; rows of every magnitude share a tile."""
+    c = Case(L, [500], [new], 8, 1, 128, BF16, E4M3)
+    c.q[:, ::2] *= 2.0 ** -125
+    c.q[:, 1] *= 2.0 ** 40
+    sm = 1e-9
+    out, lse = c.run(sm_scale=sm)
+    no_error(L)
+    r = c.ref(0, 0, sm)
+    keep = [0, 2, 3, 4, 5, 6, 7]
+    ref.assert_attended(out[:, keep], tuple(x[:, keep] for x in r), lse[:, keep], F16)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
