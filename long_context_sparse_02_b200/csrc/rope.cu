@@ -365,7 +365,9 @@ dsa_status launch_move(MoveParams &p, int T_tokens, int sm_count, cudaStream_t s
     const unsigned blocks = (unsigned)((T_tokens + p.per_block - 1) / p.per_block);
     const size_t smem = (size_t)p.per_block * (p.dim / 2) * sizeof(float2);
     auto fn = move_heads_kernel<T, VEC, INTER>;
-    if (smem > 48 * 1024 && !ensure_smem(reinterpret_cast<const void *>(fn), (int)smem)) return DSA_ERR_UNSUPPORTED;
+    // (without asking, a kernel has 48 KB, its static shared memory among them)
+    if (smem + sizeof(Dest) * MAX_TOKENS > 48 * 1024 && !ensure_smem(reinterpret_cast<const void *>(fn), (int)smem))
+        return DSA_ERR_UNSUPPORTED;
     fn<<<dim3(blocks, (unsigned)split), ROPE_THREADS, smem, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

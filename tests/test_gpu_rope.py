@@ -270,3 +270,15 @@ def test_append_skips(L):
     run([1], [999])
     no_error(L, L.DEVERR_PAGE)
     assert not vc.any()
+
+
+@pytest.mark.parametrize("dim", [12160, 12176, 12288, 12304, 50000])
+def test_wide_rotations(L, dim):
+    """Sines and cosines around the shared memory that a kernel has without asking."""
+    g = gen(dim)
+    q = randn(g, 3, 2, dim)
+    freq = L.rope_frequencies(dim)[0].cuda()
+    pos = torch.tensor([0, 7, 100000], device="cuda", dtype=torch.int32)
+    got, _ = L.rope(q, pos, L.rope_spec(freq))
+    no_error(L)
+    ref.assert_rotated(got, ref.rotate(q, pos, freq), q)
