@@ -388,7 +388,8 @@ dsa_status dsa_rope_frequencies(int32_t dim, double base, int32_t scheme, double
 /* Rotates T tokens' queries and, in the same launch, keys.  Element (t, h, d)
  * of an array lies at t*token_stride + h*head_stride + d elements, so slices of
  * one fused projection need no copy.
- *   q      device bf16 or fp16 (dtype), Hq heads of D;  q_out as q; the same
+ *   q      device bf16 or fp16 (dtype), Hq heads of D (a stride of 0 gives one to
+ *          all);  q_out as q, but each token and head a place of its own; the same
  *          pointer and strides rotate in place, other overlaps are not allowed
  *   k      the same with Hk heads, or NULL (Hk = 0)
  *   pos    device int32 [T]: any value

@@ -142,6 +142,12 @@ size_t ld_of(int32_t max_len) { return align_up((size_t)max_len, 4); }
 
 bool io_dtype_ok(int32_t dtype) { return dtype == DSA_BF16 || dtype == DSA_F16; }
 
+// Rotated heads go to places of their own: a stride of 0 (one head given to
+// all) is for inputs, in place it would turn the same elements again and again.
+bool apart(int64_t token_stride, int64_t head_stride, int32_t tokens, int32_t heads) {
+    return (tokens <= 1 || token_stride != 0) && (heads <= 1 || head_stride != 0);
+}
+
 dsa_status rope_spec_check(const dsa_rope_spec *r, int32_t D) {
     if (!r || !r->inv_freq || r->dim < 2 || (r->dim & 1) || r->offset < 0 || r->dim > D || r->offset > D - r->dim ||
         !isfinite(r->factor) || (r->inverse != 0 && r->inverse != 1) ||
@@ -558,6 +564,9 @@ dsa_status dsa_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride
         return DSA_ERR_INVALID_ARG;
     if (Hk && k == k_out && (k_token_stride != k_out_token_stride || k_head_stride != k_out_head_stride))
         return DSA_ERR_INVALID_ARG;
+    if ((Hq && !apart(q_out_token_stride, q_out_head_stride, T, Hq)) ||
+        (Hk && !apart(k_out_token_stride, k_out_head_stride, T, Hk)))
+        return DSA_ERR_INVALID_ARG;
     RopeArgs a{{q, q_token_stride, q_head_stride, Hq},
                {k, k_token_stride, k_head_stride, Hk},
                {q_out, q_out_token_stride, q_out_head_stride},
@@ -581,6 +590,7 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
     if ((q != nullptr) != (H > 0) || (q && (!rope || !q_out))) return DSA_ERR_INVALID_ARG;
     if (q && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
         return DSA_ERR_INVALID_ARG;
+    if (q && !apart(q_out_token_stride, q_out_head_stride, n, H)) return DSA_ERR_INVALID_ARG;
     if ((v_new != nullptr) != (cache->v != nullptr)) return DSA_ERR_INVALID_ARG;
     if (!k_new || !tok_seq || !tok_pos) return DSA_ERR_INVALID_ARG;
     AppendRopeArgs a{{k_new, k_token_stride, k_head_stride, cache->heads},

@@ -100,6 +100,15 @@ def test_rope_refused(L):
     assert call_rope(L, T=0) == 0 and call_rope(L, Hq=0, q=None, qo=None) == 0
 
 
+def test_one_place_for_several_heads_refused(L):
+    """One head given to all (a stride of 0) is an input; rotated into one place, in place or not, it is refused."""
+    for kw in (dict(qot=0), dict(qoh=0), dict(qo=P(256), qt=0, qot=0), dict(qo=P(256), qh=0, qoh=0),
+               dict(Hk=2, k=P(64), ko=P(64), kt=0, kh=128, kot=0, koh=128), dict(Hk=2, k=P(64), ko=P(512), kt=256, kh=128, kot=256)):
+        assert call_rope(L, **kw) == 1, kw
+    for kw in (dict(qot=0), dict(qoh=0), dict(qo=P(256), qt=0, qot=0)):
+        assert call_append(L, **dict(q=P(256), H=4, qo=P(512), qt=512, qh=128, qot=512, qoh=128) | kw) == 1, kw
+
+
 def test_append_refused(L):
     for s in BAD_SPECS:
         assert call_append(L, rope=spec(L, **s)) == 1, s
