@@ -468,6 +468,7 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  * bits each time: no atomics, a fixed order of sums.
  * Supported: Dk == Dv in {64, 128}, H a multiple of heads; T, max_q, max_len up to
  * 2^30, T * H below 2^31 - 512. */
+/* Enough for every call of at most these sizes (a window of 0 counts as the whole length). */
 size_t dsa_paged_attn_workspace_bytes(int32_t T, int32_t num_seqs, int32_t H, const dsa_kv_cache *cache,
                                       int32_t max_q, int32_t max_len, int32_t window);
 dsa_status dsa_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t H,

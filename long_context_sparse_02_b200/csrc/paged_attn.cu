@@ -585,15 +585,20 @@ bool paged_kv_maps(const dsa_kv_cache &c, int num_pages, CUtensorMap *km, CUtens
            kv_map(vm, c.v, c.dtype, c.Dk, c.heads, num_pages, c.v_page_stride, c.v_row_stride, c.v_head_stride);
 }
 
+// Enough for every call of these bounds: fewer tokens, shorter sequences or windows and fewer sequences never take more,
+// but smaller groups of heads can (a chunk's tile has 2 (128 / G) G rows), so each size of them is looked at.
 size_t paged_attn_workspace_bytes(int32_t num_seqs, int32_t H, int32_t Hkv, int32_t D, bool e4m3, int32_t max_q,
                                   int32_t max_len, int32_t window, int sm_count) {
-    const int G = H / Hkv;
-    size_t need = make_plan(tile_rows((int64_t)max_q * G, e4m3), UNIT, num_seqs, G, Hkv, D, max_q, max_len, window,
-                            sm_count).total;
-    if (tc_shape(G, max_q, e4m3)) {  // (the call's scale and strides decide between the two)
-        const size_t tc =
-            make_plan(paged_attn_tc_rows(G), 128, num_seqs, G, Hkv, D, max_q, max_len, window, sm_count).total;
-        need = tc > need ? tc : need;
+    size_t need = 0;
+    for (int G = H / Hkv; G > 0; --G) {
+        const size_t few = make_plan(tile_rows((int64_t)max_q * G, e4m3), UNIT, num_seqs, G, Hkv, D, max_q, max_len,
+                                     window, sm_count).total;
+        need = few > need ? few : need;
+        if (tc_shape(G, max_q, e4m3)) {  // (the call's scale and strides decide between the two)
+            const size_t tc =
+                make_plan(paged_attn_tc_rows(G), 128, num_seqs, G, Hkv, D, max_q, max_len, window, sm_count).total;
+            need = tc > need ? tc : need;
+        }
     }
     return need;
 }

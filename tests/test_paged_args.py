@@ -1,6 +1,7 @@
 """Rotary frequencies, and the calls that the rotating append and paged attention refuse before any CUDA call (no GPU needed)."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -150,6 +151,21 @@ def test_workspace_size(L):
     assert f(8, 8, 64, cache(L), 1, 1000, 1000) == f(8, 8, 64, cache(L), 1, 1000, 0) == f(8, 8, 64, cache(L), 1, 1000, 2 ** 31 - 1)
     # a bound, whatever the lengths: no more for a million positions than for a few thousand
     assert f(8, 8, 64, cache(L), 1, 1 << 20, 0) == f(8, 8, 64, cache(L), 1, 1 << 16, 0)
+
+
+def test_workspace_of_larger_calls_serves_smaller_ones(L):
+    """A workspace made for some sizes is enough for every call of at most these."""
+    r = random.Random(4)
+
+    def need(B, G, max_q, max_len, window, Hkv, D, dtype):
+        return L.lib.dsa_paged_attn_workspace_bytes(9, B, G * Hkv, cache(L, heads=Hkv, Dk=D, Dv=D, dtype=dtype), max_q, max_len, window)
+
+    for _ in range(3000):
+        top = (r.randint(1, 40), r.randint(1, 160), int(2 ** r.uniform(0, 11)), int(2 ** r.uniform(0, 16)), int(2 ** r.uniform(0, 17)))
+        kind = (r.choice([1, 2, 8]), r.choice([64, 128]), r.choice([0, 2]))
+        less = tuple(r.randint(1, x) if r.random() < 0.5 else x for x in top)
+        assert need(*less, *kind) <= need(*top, *kind), (less, top, kind)
+        assert need(*top, *kind) <= need(*top[:4], 0, *kind)  # (no window: all of the length)
 
 
 def test_python_checks(L):
