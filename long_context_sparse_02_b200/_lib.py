@@ -160,6 +160,9 @@ def _stream():
 
 def paged(seq_lens: torch.Tensor, block_table: torch.Tensor, num_pages: int, page_size: int = 64) -> Paged:
     """The C struct holds raw pointers, so it also keeps the two tensors alive."""
+    if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] < seq_lens.shape[0]:
+        raise ValueError(f"block_table must have a row for each of seq_lens, got {tuple(block_table.shape)} for "
+                         f"{tuple(seq_lens.shape)}")
     pg = Paged(_ptr(seq_lens, torch.int32, "seq_lens"), _ptr(block_table, torch.int32, "block_table"),
                int(seq_lens.shape[0]), int(block_table.shape[1]), int(page_size), int(num_pages))
     pg._tensors = (seq_lens, block_table)

@@ -176,3 +176,11 @@ def test_python_checks(L):
         L.kv_cache(torch.zeros(2, 64, 1, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="CUDA"):
         L.rope_spec(torch.zeros(4, dtype=torch.float64))
+
+
+def test_page_tables_have_a_row_a_sequence(L):
+    """The kernels read a row of the block table for each sequence: a table of fewer is refused before they do."""
+    lens = torch.ones(3, dtype=torch.int32)
+    for table in (torch.zeros(2, 4, dtype=torch.int32), torch.zeros(12, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="row for each"):
+            L.paged(lens, table, 8)
