@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import paged_ref as ref
-from tests.test_gpu_paged_attn import E4M3, Case
+from tests.test_gpu_paged_attn import E4M3, VS, Case
 from tests.test_gpu_rope import BF16, F16, L, gen, no_error  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -105,3 +105,69 @@ def test_tiny_queries_and_scales(L, new):  # noqa: F811
     keep = [0, 2, 3, 4, 5, 6, 7]
     ref.assert_attended(out[:, keep], tuple(x[:, keep] for x in r), lse[:, keep], F16)
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dtype,cdt,G,new", [(BF16, E4M3, 1, 3), (BF16, E4M3, 2, 6), (BF16, E4M3, 2, 45), (BF16, E4M3, 3, 300),
+                                             (BF16, None, 2, 3), (BF16, None, 2, 300)])
+def test_rows_of_every_magnitude(L, dtype, cdt, G, new):  # noqa: F811
+    """Rows of q at the ends of bf16's range, tile after tile: each is fitted by a power of two of its own."""
+    c = Case(L, [700, 900], [new, new], G, 1, 128, dtype, cdt)
+    step = torch.arange(c.T, device="cuda")
+    c.q *= (2.0 ** -((step * 37) % 90).double()).to(dtype)[:, None, None]
+    c.q[1] = 0
+    c.q[2] *= 2.0 ** -30
+    out, lse = c.run(sm_scale=0.125)
+    c.check(out, lse, 0, 0.125)
+
+
+@pytest.mark.parametrize("dtype,cdt,H,Hkv,new,n", [(BF16, E4M3, 8, 1, 1, 70000), (F16, None, 8, 1, 4, 70000),
+                                                   (BF16, None, 8, 2, 300, 20000), (BF16, E4M3, 6, 2, 300, 20000),
+                                                   (F16, E4M3, 5, 1, 300, 20000)])
+def test_same_bits_each_time(L, dtype, cdt, H, Hkv, new, n):  # noqa: F811
+    """Tiles split over many CTAs, in each kernel: the workspace's contents and what ran before leave no trace."""
+    c = Case(L, [n], [new], H, Hkv, 128, dtype, cdt)
+    out, lse = c.run()
+    ws = L.paged_attn_workspace(new, H, c.cache, c.pg, new, n).fill_(0xFF)
+    other = Case(L, [900], [400], 8, 1, 128, dtype, cdt, seed=1)
+    for _ in range(3):
+        other.run(q=other.q * 100)
+        o2, l2 = c.run(ws=ws)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    no_error(L)
+
+
+@pytest.mark.parametrize("octaves", [3.0, 0.7, 40.0])
+@pytest.mark.parametrize("dtype,cdt,G,new", KERNELS)
+def test_scores_that_grow(L, dtype, cdt, G, new, octaves):  # noqa: F811
+    """Scores that rise by `octaves` every 128 keys: the weights' reference follows, at once or after a while, and no
+    weight leaves the range of the products' type."""
+    D, n = 128, 2048
+    c = Case(L, [n], [new], G, 1, D, dtype, cdt)
+    pages = c.table[0].long()
+    ks = 24.0 if cdt else 1.0  # codes up to 24 x 17 = 408 of 448
+    k = ((torch.arange(n, device="cuda") / 128 + 1)[:, None] * torch.ones(D, device="cuda") * ks).to(c.cdt)
+    bits = torch.uint8 if cdt else c.cdt
+    c.k.view(bits)[pages] = k.reshape(-1, 64, 1, D).view(bits)
+    c.cache = L.kv_cache(c.k, c.v, ks, VS)
+    c.q.fill_(1.0)
+    sm = octaves * math.log(2) / D
+    out, lse = c.run(sm_scale=sm)
+    no_error(L)
+    kd, vd = ref.gather(c.k, c.table[0], n, ks), ref.gather(c.v, c.table[0], n, VS)
+    want = ref.attend(c.q[:new], kd, vd, torch.arange(n - new, n, device="cuda"), 0, sm)
+    ref.assert_attended(out, want, lse, F16 if cdt else None)
+
+
+@pytest.mark.parametrize("H,Hkv,window,cdt", [(4, 1, 0, None), (4, 1, 0, E4M3), (2, 2, 100, None)])
+def test_many_chunks(L, H, Hkv, window, cdt):  # noqa: F811
+    """More sequences than one pass of the planner holds, in the chunk kernel."""
+    g = torch.Generator().manual_seed(6)
+    lens = [int(x) for x in torch.randint(0, 300, (2100,), generator=g)]
+    new = [min(int(x), n + 1) for x, n in zip(torch.randint(0, 41, (2100,), generator=g), lens)]
+    c = Case(L, lens, new, H, Hkv, 64, BF16, cdt)
+    out, lse = c.run(window)
+    no_error(L)
+    for b in list(range(0, 2100, 97)) + [1023, 1024, 1025, 2047, 2048, 2099]:
+        at, m = int(c.q_start[b]), new[b]
+        if m:
+            ref.assert_attended(out[at:at + m], c.ref(b, window), lse[at:at + m], F16 if cdt else None)

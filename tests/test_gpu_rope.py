@@ -282,3 +282,31 @@ def test_wide_rotations(L, dim):
     got, _ = L.rope(q, pos, L.rope_spec(freq))
     no_error(L)
     ref.assert_rotated(got, ref.rotate(q, pos, freq), q)
+
+
+def test_latent_rows_for_the_sparse_layer(L):
+    """The layer's latent cache as a cache of one head: rows appended rotated are the rows rotated and then appended, and
+    the sparse attention over them is the same."""
+    g = gen(31)
+    seq_lens, table, pages = paged_case(g, [300, 70])
+    pg = L.paged(seq_lens, table, pages)
+    n, H, K = 40, 16, 64
+    tok_seq = torch.tensor([0] * 30 + [1] * 10, device="cuda", dtype=torch.int32)
+    tok_pos = torch.tensor([*range(270, 300), *range(60, 70)], device="cuda", dtype=torch.int32)
+    freq = L.rope_frequencies(64)[0].cuda()
+    spec = L.rope_spec(freq, offset=512, interleaved=True)
+    latent = randn(g, n, 1, 576)
+    a = randn(g, pages, 64, 576)
+    b = a.clone()
+    L.append_rope(latent, None, tok_seq, tok_pos, pg, L.kv_cache(a.unsqueeze(2)), spec)
+    turned, _ = L.rope(latent, tok_pos, spec)
+    codes = torch.zeros(pages, 64, 64, device="cuda", dtype=torch.uint8)
+    L.append_kv(randn(g, n, 64), 1.0, turned[:, 0].contiguous(), tok_seq, tok_pos, pg, codes, b)
+    no_error(L)
+    assert torch.equal(a, b)
+    idx = torch.arange(K, device="cuda", dtype=torch.int32).repeat(2, 1)
+    q, _ = L.rope(randn(g, 2, H, 576), seq_lens - 1, spec)
+    gate = randn(g, 2, H)
+    out = [L.sparse_attn(q, x, pg, None, idx, gate, 576 ** -0.5, 512) for x in (a, b)]
+    no_error(L)
+    assert torch.equal(*out) and torch.isfinite(out[0].float()).all()
