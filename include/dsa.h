@@ -462,7 +462,7 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  * A page outside [0, num_pages) reads as zeros and sets DSA_DEVERR_PAGE.
  * Softmax statistics and sums are fp32; the softmax weights enter the second
  * product in the q type (fp16 for an E4M3 cache), one rounding each; of fp16
- * ones, what lies 2^-36 below a row's largest is lost.  Over an E4M3 cache bf16
+ * ones, what lies 2^-35 below a row's largest is lost.  Over an E4M3 cache bf16
  * rows of q enter the first product in fp16, times a power of two: what lies
  * 2^-24 below the row's largest element is lost.  The same call gives the same
  * bits each time: no atomics, a fixed order of sums.

@@ -632,6 +632,7 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     p.locked = !tc && c.heads > 1 && even * 20 >= pl.nc * 19;
     const int nc = p.locked ? even : pl.nc;
     p.scale_log2 = (float)(a.sm_scale * 1.4426950408889634 / (e4m3 ? c.k_scale : 1.f));
+    if (tc) p.scale_log2 = fmaxf(p.scale_log2, PAGED_MIN_SCALE);
     p.v_inv = e4m3 ? 1.f / c.v_scale : 1.f;
     p.out = a.out, p.lse = a.lse;
     p.part_o = reinterpret_cast<float *>(ws + pl.o_off);

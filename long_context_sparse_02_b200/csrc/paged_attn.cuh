@@ -45,6 +45,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
 // Maps of the cache's keys and values: a box is one page's 64 rows of one head, up to 128 bytes wide.
 bool paged_kv_maps(const dsa_kv_cache &c, int num_pages, CUtensorMap *km, CUtensorMap *vm);
 
+// The scale of a row of the tensor-core kernel stays above 0, where the first maximum would not count as grown and the
+// reference not leave -inf.  Only 8-bit caches come near it (a division by their scale, and by the row's power of two),
+// whose scores are below 2^33: less than 2^-80 in octaves, and 0 either way.
+constexpr float PAGED_MIN_SCALE = 1e-37f;
+
 // The tensor-core kernel for chunks (paged_attn_tc.cu): rows of its tiles, and its launch.
 int paged_attn_tc_rows(int G);
 dsa_status launch_paged_attn_tc(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st);

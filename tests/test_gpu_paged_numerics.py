@@ -39,7 +39,7 @@ def test_rows_that_are_not_there(L, G, cdt):  # noqa: F811
 @pytest.mark.parametrize("dtype,cdt,G,new", KERNELS)
 def test_concentrated_weights(L, dtype, cdt, G, new, depth):  # noqa: F811
     """One key in 32 holds nearly all of the weight and has a value of 0; the others, `depth` octaves below, make the
-    output.  A weight is rounded once to the products' type; of fp16's, what lies 36 octaves below the largest is lost."""
+    output.  A weight is rounded once to the products' type; of fp16's, what lies 35 octaves below the largest is lost."""
     D, n = 128, 4096
     c = Case(L, [n], [new], G, 1, D, dtype, cdt)
     pages = c.table[0].long()
@@ -64,10 +64,11 @@ def test_concentrated_weights(L, dtype, cdt, G, new, depth):  # noqa: F811
         w = torch.exp(s[:m] - s[:m].max())
         want = (w @ vd[:m]) / w.sum()
         half = ref.HALF_STEP[F16 if cdt else dtype]
-        # weights: one rounding, and 2^-37 of the largest (half a step of fp16's smallest, lifted); scores: an fp32 product
-        # of D terms, as in assert_attended; the output's rounding, also among fp16's smallest numbers
+        # weights: one rounding, and 2^-35 of the largest (half of fp16's smallest step, 2^-25, of weights that are lifted
+        # by 2^10 at least); scores: an fp32 product of D terms, as in assert_attended; the output's rounding, also among
+        # fp16's smallest numbers
         ds = (D + 4) * 2.0 ** -24 * float((kd[:m].abs().sum(-1) * sm).max())
-        tol = (half + 2 * ds + 2.0 ** -18 + ref.HALF_STEP[dtype]) * 1.01 * want + 2.0 ** -36 * vd[:m].sum(0) / w.sum() + 2.0 ** -25
+        tol = (half + 2 * ds + 2.0 ** -18 + ref.HALF_STEP[dtype]) * 1.01 * want + 2.0 ** -35 * vd[:m].sum(0) / w.sum() + 2.0 ** -25
         err = (out[t].double() - want).abs()
         assert (err <= tol).all(), f"{float((err / want).max())} of the output"
         e = (lse[t].double() - torch.logsumexp(s[:m], 0)).abs()
