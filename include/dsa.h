@@ -353,8 +353,9 @@ dsa_status dsa_append_kv_mx(const uint16_t *k_new, const uint16_t *latent_new,
  * p * inv_freq[i], formed in fp64 and reduced to one turn before its sine and
  * cosine are taken in fp32, so far positions lose nothing:
  *   (a, b) -> factor * (a cos - b sin, b cos + a sin);  inverse: sin -> -sin
- * (with factor 1 the inverse is the transpose: it undoes the rotation, and
- * takes a gradient through it).  Pairs are elements (i, i + dim/2) of the part
+ * (the inverse is the transpose: it takes a gradient through the rotation, and
+ * with factor 1 it undoes it; a rotation of another factor is undone by the
+ * inverse with 1 / factor).  Pairs are elements (i, i + dim/2) of the part
  * (DSA_ROPE_HALF) or (2i, 2i + 1) (DSA_ROPE_INTERLEAVED).  Elements of a head
  * outside [offset, offset + dim) are copied.  Results are rounded once, from
  * fp32. */
@@ -374,10 +375,10 @@ typedef struct {
  * `scale` times as long as the `orig_len` positions of training, and the
  * factor that goes with them (1 but for YaRN).  Published schemes:
  *   DSA_ROPE_PLAIN   unchanged (scale and orig_len are not looked at);
- *   DSA_ROPE_LINEAR  position interpolation: every frequency / scale;
- *   DSA_ROPE_NTK     base * scale^(dim/(dim-2)): the slowest pair stretches by
+ *   DSA_ROPE_LINEAR  position interpolation (Chen et al. 2023): every frequency / scale;
+ *   DSA_ROPE_NTK     "NTK-aware" (bloc97, 2023): base * scale^(dim/(dim-2)): the slowest pair stretches by
  *                    scale, the fastest stays (dim > 2);
- *   DSA_ROPE_YARN    pairs of over 32 turns within orig_len stay, those of under
+ *   DSA_ROPE_YARN    YaRN (Peng et al. 2023): pairs of over 32 turns within orig_len stay, those of under
  *                    one are divided by scale, a linear ramp over the pair index
  *                    between (bounds rounded outward); factor 0.1 ln(scale) + 1.
  * inv_freq_host: host fp64 [dim/2]; factor: host. base > 1, scale >= 1. */
@@ -456,7 +457,8 @@ dsa_status dsa_append_rope(const void *k_new, int64_t k_token_stride, int64_t k_
  *            decode, query t is the last token of sequence t, T == num_seqs
  *   max_q, max_len  host bounds on n_b and seq_lens: a sequence over either, or
  *            with q_start out of order, is skipped and sets DSA_DEVERR_SHAPE
- *   out      device dtype [T, H, Dv] dense;  lse device fp32 [T, H] or NULL
+ *   out      device dtype [T, H, Dv] dense, none of the inputs' memory;  lse device
+ *            fp32 [T, H] or NULL
  *   ws       dsa_paged_attn_workspace_bytes() bytes, 256-byte aligned; contents
  *            need no initialisation; calls that may overlap need one each
  * A page outside [0, num_pages) reads as zeros and sets DSA_DEVERR_PAGE.

@@ -450,7 +450,8 @@ def rope_frequencies(dim: int, base: float = 10000.0, scheme: str = "plain", sca
 
 def rope_spec(inv_freq: torch.Tensor, offset: int = 0, interleaved: bool = False, inverse: bool = False,
               factor: float = 1.0) -> RopeSpec:
-    """inv_freq fp64 [dim/2] on the GPU; elements offset .. offset + dim of each head are rotated.  Keeps inv_freq alive."""
+    """inv_freq fp64 [dim/2] on the GPU; elements offset .. offset + dim of each head are rotated.  `inverse` is the
+    transpose, a gradient's way back; to undo a rotation of some factor, give the inverse 1 / factor.  Keeps inv_freq alive."""
     spec = RopeSpec(_ptr(inv_freq, torch.float64, "inv_freq"), 2 * int(inv_freq.numel()), int(offset),
                     ROPE_INTERLEAVED if interleaved else ROPE_HALF, int(bool(inverse)), float(factor))
     spec._tensors = (inv_freq,)
@@ -460,7 +461,9 @@ def rope_spec(inv_freq: torch.Tensor, offset: int = 0, interleaved: bool = False
 
 def kv_cache(k: torch.Tensor, v: torch.Tensor = None, k_scale: float = 1.0, v_scale: float = 1.0) -> KvCache:
     """A paged cache [pages, 64, heads, width] of keys and (optionally) values: bf16, fp16, or e4m3 codes of value * scale
-    (uint8 or float8_e4m3fn).  Any strides with a contiguous last dimension.  Keeps both tensors alive."""
+    (uint8 or float8_e4m3fn).  Any strides with a contiguous last dimension.  The sparse layer's latent cache
+    [pages, 64, 576] is kv_cache(latents.unsqueeze(2)): append_rope then writes the latent rows, rotated, and append_kv,
+    given no latent rows, the indexer keys alone.  Keeps both tensors alive."""
     for name, t in (("k", k), ("v", v)):
         if t is None:
             continue
@@ -546,7 +549,7 @@ def paged_attn_workspace(T: int, H: int, cache: KvCache, pg: Paged, max_q: int, 
 def paged_attn(q, cache: KvCache, pg: Paged, q_start, max_q: int, max_len: int, window: int = 0, sm_scale: float = None,
                want_lse: bool = False, out=None, lse=None, ws=None):
     """Attention of q [T, H, D], each sequence's newest tokens (rows q_start[b] .. q_start[b+1], int32 [num_seqs + 1]; None:
-    one each), over the paged cache, causal, optionally within a window.  Returns out, or (out, lse) with want_lse."""
+    one each), over the paged cache, causal, optionally within a window.  Returns out, or (out, lse) with want_lse or lse."""
     dev, dtype, T, H, D = _first(q, "q")
     _cache_fits(cache, pg, dev)
     if D != cache.Dk:

@@ -9,17 +9,18 @@
 // With few rows the bound is HBM: a K/V head's keys and values are read once
 // for all its query heads (rows are packed: see paged_plan.cuh).  One CTA per
 // SM: a producer warp keeps a ring of units (64 positions = one page, K and V)
-// full by TMA, 160 KB in flight per SM; eight consumer warps take slices of 32
+// full by TMA, 128 KB in flight per SM (160 KB of 2-byte caches of 128-wide heads); eight consumer warps take slices of 32
 // or 16 keys in turn, each with the running statistics and the output of its
 // 16 rows in registers, and join at the end of a tile in a fixed order.  Keys
 // and values go from swizzled shared memory to the fragments by ldmatrix; an
 // 8-bit cache is widened to fp16 (exact) in registers, one conversion for two
-// values, and the rows of q are scaled by a power of two to fit fp16 exactly.
+// values, and bf16 rows of q are scaled by a power of two into fp16, which loses
+// what lies 2^-24 below a row's largest element.
 //
 // Measured: 64 sequences of 4096-65536 positions, one token each, 64 heads of
-// 128 on 8, bf16: 1230 us for 8.95 GB (above the measured copy rate, which has
-// writes in it); four drafts of 8 sequences 605 us; one token over 4097
-// positions 15 us on the device.
+// 128 on 8, bf16: 1230 us in short runs, 1262 in long ones, for 8.95 GB (above
+// the measured copy rate, which has writes in it); four drafts of 8 sequences of
+// 131072 positions 610 and 750 us; one token over 4097 positions 15 us.
 #include <cuda_fp16.h>
 
 #include "dsa_device.cuh"
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_attn_join_kernel(const 
 // Rows of a tile: enough 16-row groups for one sequence's packed rows, up to
 // 128; up to eight rows over an 8-bit cache have a kernel of their own, in which
 // they are columns (33 sequences of 1000-40000 positions, one token of 8 heads a
-// K/V head: 252 us, 268 in long runs, against 257 and 287 as half of a 16-row tile).
+// K/V head, in short runs: 252 us against 257 as half of a 16-row tile; the gap was wider in long ones).
 int tile_rows(int64_t max_rows, bool e4m3) {
     if (e4m3 && max_rows <= 8) return 8;
     int mt = 1;
@@ -564,6 +565,13 @@ dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cuda
     return launch_kw<D, IO_F16, E4M3, 32>(a, p, nc, st);
 }
 
+template <int D>
+dsa_status launch(const PagedAttnArgs &a, const PagedAttnParams &p, int nc, cudaStream_t st) {
+    const bool f16 = a.dtype == DSA_F16;
+    if (a.cache->dtype == DSA_E4M3) return f16 ? launch<D, true, true>(a, p, nc, st) : launch<D, false, true>(a, p, nc, st);
+    return f16 ? launch<D, true, false>(a, p, nc, st) : launch<D, false, false>(a, p, nc, st);
+}
+
 template <int D, bool IO_F16>
 dsa_status launch_join(const PagedAttnParams &p, int nc, cudaStream_t st) {
     if (nc == 1) return DSA_OK;  // one CTA holds every tile whole
@@ -626,7 +634,7 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     // against 192).
     p.align = tc && a.window && p.G == 1 ? 128 : 0;
     // Heads in step, where that idles no more than one CTA in twenty: 64 sequences' decode 1230 us against 1280,
-    // an 8-bit cache 252 against 284, drafts 605 against 630.  Chunks, whose keys come from L2, were slower (1658
+    // an 8-bit cache 252 against 284, drafts 605 against 630, in short runs.  Chunks, whose keys come from L2, were slower (1658
     // against 1634).
     const int even = pl.nc / c.heads * c.heads;
     p.locked = !tc && c.heads > 1 && even * 20 >= pl.nc * 19;
@@ -641,12 +649,10 @@ dsa_status launch_paged_attn(const PagedAttnArgs &a, cudaStream_t st) {
     p.err = dev->err;
     const bool f16 = a.dtype == DSA_F16;
     dsa_status s;
-#define DSA_PAGED(D_)                                                                        (f16 ? (e4m3 ? launch<D_, true, true>(a, p, nc, st) : launch<D_, true, false>(a, p, nc, st))          : (e4m3 ? launch<D_, false, true>(a, p, nc, st) : launch<D_, false, false>(a, p, nc, st)))
     if (tc)
         s = launch_paged_attn_tc(a, p, nc, st);
     else
-        s = D == 128 ? DSA_PAGED(128) : DSA_PAGED(64);
-#undef DSA_PAGED
+        s = D == 128 ? launch<128>(a, p, nc, st) : launch<64>(a, p, nc, st);
     if (s != DSA_OK) return s;
     if (D == 128) return f16 ? launch_join<128, true>(p, nc, st) : launch_join<128, false>(p, nc, st);
     return f16 ? launch_join<64, true>(p, nc, st) : launch_join<64, false>(p, nc, st);

@@ -7,8 +7,8 @@
 // exponentials halve, so that sixteen warps a CTA fit, and the widening of the
 // codes (two conversions a pair of elements, most of the instructions) hides
 // behind the loads.  HBM-bound by intent: 33 sequences of 1000-40000
-// positions, 64 heads of 128 on 8: 252 us in short runs, 268 in long ones, for
-// 1.43 GB (87% and 81% of the measured copy rate; a page's rows lie 128 bytes a
+// positions, 64 heads of 128 on 8: 256 us in short runs, 276 in long ones, for
+// 1.43 GB (85% and 79% of the measured copy rate; a page's rows lie 128 bytes a
 // head apart, and heads read in step find them together: 284 us out of step).
 #include "dsa_device.cuh"
 #include "dsa_internal.h"

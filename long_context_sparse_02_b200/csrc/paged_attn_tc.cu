@@ -23,12 +23,12 @@
 // tensor copies whose box is a row block; queries and scores never touch
 // registers before the softmax.
 //
-// 4096 tokens over 32768 positions, 32 heads of 128 on 4, bf16: 1610 us in
-// short runs (1280 TFLOP/s, 77% of the measured burst rate; 3650 clocks a unit
-// of which the tensor pipe is busy 2048), 1900 under the power cap.  What it
+// 4096 tokens over 32768 positions, 32 heads of 128 on 4, bf16: 1610-1690 us in
+// short runs (1220-1280 TFLOP/s, 74-77% of the measured burst rate; 3650 clocks a unit
+// of which the tensor pipe is busy 2048), 1920 under the power cap.  What it
 // waits for is a row block's chain: scores 512 clocks, exponentials 1024 (16 a
 // clock), product 512, and the reads and signals between.  An E4M3 cache: the
-// wideners keep up at 2145 us.
+// wideners keep up at 2145-2190 us.
 #include <cuda_fp16.h>
 
 #include "dsa_device.cuh"

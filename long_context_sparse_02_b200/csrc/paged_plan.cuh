@@ -16,8 +16,9 @@
 // every head has a line of its own and the CTAs of one part of all of them read
 // the same pages at the same time, so that the rows of a page, which lie
 // interleaved by heads, come from memory together.  Lengths are read on the device: every CTA
-// sums the units itself (a few thousand instructions at most), and its result
-// depends on nothing but the lengths.
+// sums the units of all sequences itself, tile by tile where a sequence has several, and again to find its place where
+// there are more than 1024 sequences; a cost that grows with both, spread over the block's warps.  The result depends
+// on nothing but the lengths.
 #pragma once
 
 #include "dsa_device.cuh"
